@@ -435,6 +435,89 @@ sl_status sl_sampler_generate(sl_sampler *s, const int32_t *h_prompts, int32_t *
 sl_status sl_sampler_get_state(const sl_sampler *s, sl_sampler_state *out);
 void sl_sampler_destroy(sl_sampler *s);
 
+/* ------------------------------------------------- key-set attention --- */
+
+/* Attention of the active rows over a key set per sequence, the attention
+ * weight each cached key receives from them, and eviction from the cache by
+ * that weight.  The pages cache K/V of every locked position for the whole
+ * decode and let each active row attend to all N of them (Paper-Notes,
+ * "permanent locking"; gist.science/nl section 2, O(M N d)); these entry points
+ * are library-level: they cut N to the entries that are still looked at, and
+ * read a prompt shared by the batch once.  They take pointers to any cache of
+ * [batch * n_ctx][ld] rows (sl_kv_cache_view gives such pointers), with K/V
+ * heads that several query heads may share.
+ *
+ * The object owns a workspace and serves one call at a time (one stream, or
+ * streams the caller orders); calls allocate nothing, read offsets and lengths
+ * on the device and may be captured into CUDA graphs.  It belongs to the device
+ * that is current when it is created; calls on another return SL_ERR_INVALID. */
+typedef struct sl_key_attn sl_key_attn;
+typedef struct sl_key_attn_config {
+  int dtype;             /* sl_dtype of q, k, v and o */
+  int batch, n_ctx;      /* sequences (1..SL_MAX_BATCH); cache rows of each */
+  int max_rows;          /* most query rows of a call */
+  int n_heads;           /* query heads, a multiple of n_kv_heads (64 times at most) */
+  int n_kv_heads;        /* head h reads K/V head h * n_kv_heads / n_heads */
+  int head_dim;          /* up to 128, 16-byte multiples (bf16 64 and 128: tensor cores) */
+  int prefix;            /* 1: calls may pass a prefix shared by the batch */
+  float scale;           /* score scale; 0 = 1 / sqrt(head_dim) */
+} sl_key_attn_config;
+/* SL_ERR_INVALID / SL_ERR_UNSUPPORTED on sizes outside the above, SL_ERR_OOM if
+ * the workspace cannot be allocated (about 40 MB for bf16 heads of 128, and with
+ * `prefix` 1 KB more per row and head for up to 96 * batch rows). */
+sl_status sl_key_attn_create(const sl_key_attn_config *cfg, sl_key_attn **out);
+void sl_key_attn_destroy(sl_key_attn *a);
+
+/* Query rows and key set of each sequence, on the device.  Rows of sequence b
+ * are seq_off[b] .. seq_off[b + 1] (ascending, as sl_active_view gives them;
+ * offsets outside [0, rows] are clamped).  Its keys are the cache entries
+ * keys[b][0 .. key_len[b]) (positions in [0, n_ctx); sl_kv_evict writes such
+ * lists), or entries 0 .. key_len[b] where keys is NULL; key_len NULL means n_ctx
+ * of them, and lengths outside [0, n_ctx] are clamped.  A position named twice
+ * counts as two keys.  A position outside [0, n_ctx) stands for a key and value
+ * of zeros and is reported by sl_device_check (SL_ERR_STATE). */
+typedef struct sl_key_set {
+  const int32_t *d_seq_off; /* [batch + 1] */
+  const int32_t *d_key_len; /* [batch] or NULL */
+  const int32_t *d_keys;    /* [batch][n_ctx] or NULL */
+} sl_key_set;
+
+/*   o_jh = sum_n p_jhn v_n,  p_jhn = exp(scale q_jh . k_n - lse_jh),
+ *   lse_jh = log sum_n exp(scale q_jh . k_n)
+ * over the prefix_len rows of the prefix (shared by every sequence) and the
+ * row's key set.  q, o: [rows][ld >= n_heads * head_dim]; k, v:
+ * [batch * n_ctx][ld_kv >= n_kv_heads * head_dim]; prefix: [prefix_len][ld_prefix];
+ * pointers and rows 16-byte aligned.  d_lse [rows][n_heads] fp32, or NULL.  A row
+ * without keys gets o = 0, lse = -inf; rows outside every sequence are not
+ * written, and entries outside a key set are never read into a result.  o and
+ * lse must not overlap the operands.  Softmax and sums in fp32; bf16 operands
+ * round p to bf16 for the product with v. */
+sl_status sl_key_attention(sl_key_attn *a, int rows, const void *d_q, int64_t ld_q,
+                           const void *d_k, const void *d_v, int64_t ld_kv, const sl_key_set *set,
+                           const void *d_k_prefix, const void *d_v_prefix, int64_t ld_prefix,
+                           int prefix_len, void *d_o, int64_t ld_o, float *d_lse, void *stream);
+/*   mass[b][n] = decay mass_prev[b][n] + sum_h sum_{j in b} exp(scale q_jh . k_n - lse_jh)
+ * for the positions n of b's key set (the others only decay), with the lse that
+ * sl_key_attention left for these rows (prefix included): the attention weight
+ * each cached entry received, to be accumulated over layers and steps.  mass and
+ * mass_prev: [batch][n_ctx] fp32, may be the same; decay = 0 does not read
+ * mass_prev (may be NULL).  Rows with lse = -inf weigh nothing. */
+sl_status sl_key_mass(sl_key_attn *a, int rows, const void *d_q, int64_t ld_q, const void *d_k,
+                      int64_t ld_kv, const sl_key_set *set, const float *d_lse, float decay,
+                      const float *d_mass_prev, float *d_mass, void *stream);
+/* Eviction: sequence b keeps the entries that are present and protected, and of
+ * the other present ones the heaviest, ties to the lower position, until
+ * `budget` entries are kept (protected entries stay even above it).  NaN weighs
+ * as -inf.  mass [batch][n_ctx] fp32; protect, present: [batch][n_ctx] u8 or NULL
+ * (nothing protected / everything present), e.g. the rows not yet locked.
+ * Writes the kept positions ascending into keys[b][0 .. key_len[b]) (entries
+ * behind are left as they were), key_len [batch], and the new flags into
+ * present_out [batch][n_ctx] (NULL, or the same buffer as present).  Allocates
+ * nothing.  SL_ERR_UNSUPPORTED above n_ctx = 2^20. */
+sl_status sl_kv_evict(int batch, int n_ctx, int budget, const float *d_mass,
+                      const uint8_t *d_protect, const uint8_t *d_present, int32_t *d_keys,
+                      int32_t *d_key_len, uint8_t *d_present_out, void *stream);
+
 /* ------------------------------------------------------------ diagnostics --- */
 
 /* Per kernel class device time, measured with CUDA events around every launch

@@ -64,8 +64,19 @@ class Timing(C.Structure):
                 ("kernels", C.c_longlong)]
 
 
+class KeyAttnConfig(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("batch", C.c_int), ("n_ctx", C.c_int),
+                ("max_rows", C.c_int), ("n_heads", C.c_int), ("n_kv_heads", C.c_int),
+                ("head_dim", C.c_int), ("prefix", C.c_int), ("scale", C.c_float)]
+
+
+class KeySet(C.Structure):
+    _fields_ = [("d_seq_off", C.c_void_p), ("d_key_len", C.c_void_p), ("d_keys", C.c_void_p)]
+
+
 _P = C.c_void_p
 _I = C.c_int
+_L = C.c_int64
 # name -> (restype, argtypes); the full exported surface of include/surelock.h
 SIGNATURES = {
     "sl_last_error": (C.c_char_p, []),
@@ -107,6 +118,12 @@ SIGNATURES = {
     "sl_model_set_tuning": (_I, [_P, _I, _I, _I, _I, _I]),
     "sl_model_set_attention": (_I, [_P, _I, _I]),
     "sl_model_set_attention_keys": (_I, [_P, _I]),
+    "sl_key_attn_create": (_I, [C.POINTER(KeyAttnConfig), C.POINTER(_P)]),
+    "sl_key_attn_destroy": (None, [_P]),
+    "sl_key_attention": (_I, [_P, _I, _P, _L, _P, _P, _L, C.POINTER(KeySet), _P, _P, _L, _I, _P,
+                              _L, _P, _P]),
+    "sl_key_mass": (_I, [_P, _I, _P, _L, _P, _L, C.POINTER(KeySet), _P, C.c_float, _P, _P, _P]),
+    "sl_kv_evict": (_I, [_I, _I, _I, _P, _P, _P, _P, _P, _P, _P]),
     "sl_timing_enable": (_I, [_P, _I]),
     "sl_timing_read": (_I, [_P, C.POINTER(Timing), _I]),
     "sl_device_check": (_I, [_I]),

@@ -791,6 +791,7 @@ static sl_status layer_f32(sl_model *m, sl_kv_cache *c, sl_active *a, int l, flo
 // Failure-detection test hooks (sl_debug_*): the wait limit of later GEMM
 // launches, and a one-shot lost operand copy in the next one.
 static std::atomic<unsigned long long> g_wait_limit_ns{0};
+unsigned long long sl::wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 static std::atomic<int> g_lost_load{0};
 
 // Split-K tile fix-up in the GEMM epilogue instead of a finalize kernel

@@ -1,0 +1,364 @@
+// Attention of the active rows over a key set per sequence: the first key_len
+// cache entries or a list of kept positions (what an eviction leaves), and a
+// prefix shared by the whole batch.
+//
+// The pages keep the keys and values of every locked position and let each
+// active row attend to all N of them, O(M N d) a step (Paper-Notes, "permanent
+// locking"; gist.science/nl section 2, "Complexiteitsvermindering").  A row's
+// key set here is what the caller kept of them:
+//   z_jhn = scale q_jh . k_n,  lse_jh = log sum_n exp(z_jhn),
+//   o_jh = sum_n exp(z_jhn - lse_jh) v_n   over the prefix and the sequence's set,
+// in one pass over the keys with a running maximum and sum.  The G = H / Hkv
+// query heads of a K/V head share its tiles: a tile's rows are (query row,
+// head of the group) pairs.  A row without keys has o = 0, lse = -inf.
+//
+// This file holds the fp32-arithmetic kernel (fp32 models, and bf16 heads the
+// tensor-core kernel does not take) and the kernel that joins partial rows.
+#include "common.cuh"
+#include "keys_common.cuh"
+#include "keys_plan.cuh"
+
+namespace sl {
+
+namespace {
+constexpr int KS_T = 64;              // packed rows and keys of a tile
+constexpr int KS_THREADS = 256;
+}  // namespace
+
+// Rows (qr, g) packed as qr * G + g; 64 packed rows against 64 keys at a time,
+// 256 threads as 16 x 16: thread (ty, tx) holds scores of rows 4 ty + i and
+// keys tx + 16 j, and of the output rows 4 ty + i the columns 4 tx + 64 c.
+// Operands are staged in shared memory as fp32 with rows padded by four floats
+// (16 rows read at a time then fall into distinct banks).  Bound by shared
+// memory reads (8 16-byte reads per 64 multiply-adds).
+template <typename T>
+__global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs a) {
+  extern __shared__ float4 ks_smem4[];
+  __shared__ KeyPlan pl;
+  float *smem = reinterpret_cast<float *>(ks_smem4);
+  const int D = a.D, ld = D + 4;
+  float *sq = smem, *sk = sq + KS_T * ld, *sv = sk + KS_T * ld, *sp = sv + KS_T * ld;
+  constexpr int LP = KS_T + 4;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, lane = tid & 31;
+  const int QR = KS_T / a.G;                        // query rows of a unit
+  pdl_wait();
+  if (tid < 32) key_plan_build(pl, a, QR, KS_T, gridDim.x, false, lane);
+  __syncthreads();
+  pdl_trigger();
+  const int tp = kp_tiles(a.prefix_len, KS_T);
+  const int d4 = D >> 2;
+  const float c2 = a.scale * KEY_LOG2E;
+
+  int w = min((long long)blockIdx.x * pl.chunk, (long long)pl.wbase[pl.njobs]), job = 0;
+  const int w_end = min((long long)w + pl.chunk, (long long)pl.wbase[pl.njobs]);
+  KeyPiece pc;
+  while (key_next(pl, a.Hkv, w, w_end, job, pc)) {
+    const int b = kp_seq(pl, pc.job);
+    const int r0 = (b < 0 ? pl.q0[0] : pl.q0[b]) + pc.unit * QR;
+    const int rn = min(QR, (b < 0 ? pl.q0[a.batch] : pl.q0[b + 1]) - r0) * a.G;   // packed rows
+    __syncthreads();
+    for (int i = tid; i < KS_T * d4; i += KS_THREADS) {
+      const int r = i / d4, c = (i - r * d4) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rn)
+        v = load4((const T *)a.q + (r0 + r / a.G) * a.ld_q + (pc.hk * a.G + r % a.G) * D + c);
+      *reinterpret_cast<float4 *>(sq + r * ld + c) = v;
+    }
+    float m[4], l[4];
+    float4 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      acc[i][0] = acc[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int t = pc.t0; t < pc.t1; ++t) {
+      // the tile's keys: of the prefix, then of the sequence's own set
+      const bool pre = b < 0 || (!pl.stacked && t < tp);
+      const int i0 = (pre || pl.stacked ? t : t - tp) * KS_T;
+      const int nv = min(KS_T, (pre ? a.prefix_len : pl.kl[b]) - i0);
+      __syncthreads();
+      for (int i = tid; i < KS_T * d4; i += KS_THREADS) {
+        const int r = i / d4, c = (i - r * d4) * 4;
+        float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
+        if (r < nv) {
+          const int pos = pre ? i0 + r : key_pos(a, b, i0 + r);
+          if (pos >= 0) {
+            const long long off = pre ? pos * a.ld_p + pc.hk * D + c
+                                      : ((long long)b * a.n_ctx + pos) * a.ld_kv + pc.hk * D + c;
+            kv = load4((const T *)(pre ? a.kp : a.k) + off);
+            vv = load4((const T *)(pre ? a.vp : a.v) + off);
+          }
+        }
+        *reinterpret_cast<float4 *>(sk + r * ld + c) = kv;
+        *reinterpret_cast<float4 *>(sv + r * ld + c) = vv;
+      }
+      __syncthreads();
+      float s[4][4] = {};
+      for (int c = 0; c < D; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * ld + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * ld + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+            s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+            s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+            s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float mt = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = tx + 16 * j < nv ? s[i][j] * c2 : -INFINITY;
+          mt = fmaxf(mt, s[i][j]);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+        const float mn = fmaxf(m[i], mt);
+        const float ms = mn == -INFINITY ? 0.f : mn;      // no finite score yet: all p = 0
+        const float al = exp2f(m[i] - ms);                // 2^-inf = 0 at the first tile
+        float rs = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p = exp2f(s[i][j] - ms);
+          sp[(4 * ty + i) * LP + tx + 16 * j] = p;
+          rs += p;
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
+        l[i] = l[i] * al + rs;
+        m[i] = mn;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          acc[i][c].x *= al;
+          acc[i][c].y *= al;
+          acc[i][c].z *= al;
+          acc[i][c].w *= al;
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int col = 4 * tx + 64 * c;
+        if (col >= D) continue;
+        for (int n = 0; n < KS_T; n += 4) {
+          float4 p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(sp + (4 * ty + i) * LP + n);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 v = *reinterpret_cast<const float4 *>(sv + (n + e) * ld + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float pe = e == 0 ? p[i].x : e == 1 ? p[i].y : e == 2 ? p[i].z : p[i].w;
+              acc[i][c].x = fmaf(pe, v.x, acc[i][c].x);
+              acc[i][c].y = fmaf(pe, v.y, acc[i][c].y);
+              acc[i][c].z = fmaf(pe, v.z, acc[i][c].z);
+              acc[i][c].w = fmaf(pe, v.w, acc[i][c].w);
+            }
+          }
+        }
+      }
+    }
+    // whole unit of a sequence's full key list: final rows; else partial ones
+    const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
+    const size_t slot_f = (size_t)KS_T * (D + 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * ty + i;
+      if (r >= rn) continue;
+      const int row = r0 + r / a.G, h = pc.hk * a.G + r % a.G;
+      if (whole && !pl.stacked) {
+        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          if (4 * tx + 64 * c < D)
+            store4((T *)a.o + row * a.ld_o + h * D + 4 * tx + 64 * c,
+                   make_float4(acc[i][c].x * inv, acc[i][c].y * inv, acc[i][c].z * inv,
+                               acc[i][c].w * inv));
+        if (a.lse && tx == 0)
+          a.lse[(size_t)row * a.H + h] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * KEY_LN2;
+        continue;
+      }
+      float *rec;
+      if (whole)
+        rec = a.ws + 2 * (size_t)gridDim.x * slot_f +
+              (((size_t)(b < 0 ? 0 : 1) * a.M + row) * a.H + h) * (D + 2);
+      else
+        rec = a.ws + kp_slot(blockIdx.x, pc.t0) * slot_f + (size_t)r * (D + 2);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (4 * tx + 64 * c < D) {
+          float2 *dst = reinterpret_cast<float2 *>(rec + 2 + 4 * tx + 64 * c);
+          dst[0] = make_float2(acc[i][c].x, acc[i][c].y);
+          dst[1] = make_float2(acc[i][c].z, acc[i][c].w);
+        }
+      if (tx == 0) *reinterpret_cast<float2 *>(rec) = make_float2(m[i], l[i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- joining --
+// Partial rows (max m in base 2, sum l, unnormalised o) of one (row, head)
+// joined in the order of the CTAs that left them: o = sum_i 2^(m_i - m) o_i / L,
+// L = sum_i 2^(m_i - m) l_i.  One warp per (row, head), lanes over the columns.
+// Without a joint prefix only units that a CTA's share cut have partial rows:
+// blockIdx.x = c looks at the cut at the start of CTA c's share, and the first
+// cut of a unit joins it, blockIdx.y sharing its rows.  With one, every row
+// does (one part from the prefix, one from its sequence's own keys).
+struct JoinAcc {
+  float m, l;
+  float4 o;
+};
+
+__device__ __forceinline__ void join_rec(JoinAcc &x, const float *rec, int D, int lane) {
+  const float2 ml = __ldcg(reinterpret_cast<const float2 *>(rec));
+  const float mn = fmaxf(x.m, ml.x);
+  const float ms = mn == -INFINITY ? 0.f : mn;
+  const float ca = exp2f(x.m - ms), cb = exp2f(ml.x - ms);
+  x.l = x.l * ca + ml.y * cb;
+  x.m = mn;
+  if (4 * lane < D) {
+    const float2 u = __ldcg(reinterpret_cast<const float2 *>(rec + 2 + 4 * lane));
+    const float2 v = __ldcg(reinterpret_cast<const float2 *>(rec + 4 + 4 * lane));
+    x.o.x = x.o.x * ca + u.x * cb;
+    x.o.y = x.o.y * ca + u.y * cb;
+    x.o.z = x.o.z * ca + v.x * cb;
+    x.o.w = x.o.w * ca + v.y * cb;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void join_store(const KeyArgs &a, const JoinAcc &x, int row, int h,
+                                           int lane) {
+  const float inv = x.l > 0.f ? 1.f / x.l : (x.l == 0.f ? 0.f : x.l);
+  if (4 * lane < a.D)
+    store4((T *)a.o + row * a.ld_o + h * a.D + 4 * lane,
+           make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+  if (a.lse && lane == 0)
+    a.lse[(size_t)row * a.H + h] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * KEY_LN2;
+}
+
+// The pieces of one unit of job j (row offset inside it: packed row r).
+__device__ __forceinline__ void join_unit(const KeyArgs &a, const KeyPlan &pl, JoinAcc &x, int j,
+                                          int unit, int hk, int r, int rt, int row, int h,
+                                          int lane) {
+  const int T = pl.T[j];
+  if (T == 0) return;
+  const int wu = pl.wbase[j] + (unit * a.Hkv + hk) * (T + KP_OV);
+  const size_t slot_f = (size_t)rt * (a.D + 2);
+  const int c1 = (wu + T + KP_OV - 1) / pl.chunk;
+  for (int c = wu / pl.chunk; c <= c1; ++c) {
+    int t0, t1;
+    kp_piece_of(pl, wu, T, c, t0, t1);
+    if (t1 <= t0) continue;
+    const float *rec;
+    if (t0 == 0 && t1 == T)
+      rec = a.ws + 2 * (size_t)a.n_ctas * slot_f +
+            (((size_t)(kp_seq(pl, j) < 0 ? 0 : 1) * a.M + row) * a.H + h) * (a.D + 2);
+    else
+      rec = a.ws + kp_slot(c, t0) * slot_f + (size_t)r * (a.D + 2);
+    join_rec(x, rec, a.D, lane);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) key_join_kernel(const KeyArgs a, int rt, int uq, int kt) {
+  __shared__ KeyPlan pl;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) key_plan_build(pl, a, uq, kt, a.n_ctas, false, lane);
+  __syncthreads();
+  const int W = pl.wbase[pl.njobs];
+  const int n_warps = gridDim.x * gridDim.y * 8;
+  const int gw = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp;
+  if (pl.stacked) {
+    const int rows = pl.q0[a.batch] - pl.q0[0];
+    int b = 0;
+    for (long long i = gw; i < (long long)rows * a.H; i += n_warps) {
+      const int row = pl.q0[0] + (int)(i / a.H), h = (int)(i % a.H);
+      const int hk = h / a.G, g = h % a.G;
+      while (pl.q0[b + 1] <= row) ++b;
+      JoinAcc x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      const int rp = row - pl.q0[0], ro = row - pl.q0[b];
+      join_unit(a, pl, x, 0, rp / uq, hk, (rp % uq) * a.G + g, rt, row, h, lane);
+      join_unit(a, pl, x, b + 1, ro / uq, hk, (ro % uq) * a.G + g, rt, row, h, lane);
+      join_store<T>(a, x, row, h, lane);
+    }
+    return;
+  }
+  if (pl.empty) {
+    for (int b = 0; b < a.batch; ++b) {
+      if (pl.T[b] > 0) continue;
+      const long long n = (long long)(pl.q0[b + 1] - pl.q0[b]) * a.H;
+      for (long long i = gw; i < n; i += n_warps)
+        join_store<T>(a, JoinAcc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)},
+                      pl.q0[b] + (int)(i / a.H), (int)(i % a.H), lane);
+    }
+  }
+  const int c = blockIdx.x;
+  const long long cut = (long long)c * pl.chunk;
+  if (c == 0 || cut >= W) return;
+  int j = 0;
+  while (cut >= pl.wbase[j + 1]) ++j;
+  const int cu = pl.T[j] + KP_OV, u = ((int)cut - pl.wbase[j]) / cu;
+  const int wu = pl.wbase[j] + u * cu;
+  // the unit's first cut joins it; a cut at its start is none
+  if (cut == wu || (long long)(c - 1) * pl.chunk > wu) return;
+  if (cut - wu <= KP_OV) {
+    // the share before holds no tile of it: whole if this share ends it
+    int t0, t1;
+    kp_piece_of(pl, wu, pl.T[j], c, t0, t1);
+    if (t1 == pl.T[j]) return;
+  }
+  const int unit = u / a.Hkv, hk = u - unit * a.Hkv;
+  const int r0 = pl.q0[j] + unit * uq;
+  const int rn = min(uq, pl.q0[j + 1] - r0) * a.G;
+  for (int r = blockIdx.y * 8 + warp; r < rn; r += gridDim.y * 8) {
+    JoinAcc x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    const int row = r0 + r / a.G, h = hk * a.G + r % a.G;
+    join_unit(a, pl, x, j, unit, hk, r, rt, row, h, lane);
+    join_store<T>(a, x, row, h, lane);
+  }
+}
+
+// ---------------------------------------------------------------------- host --
+namespace {
+size_t simt_smem(int D) { return ((size_t)3 * KS_T * (D + 4) + KS_T * (KS_T + 4)) * 4; }
+
+template <typename T> cudaError_t run_simt(const KeyArgs &a, cudaStream_t s) {
+  const size_t smem = simt_smem(a.D);
+  cudaError_t e = cudaFuncSetAttribute(key_attn_simt_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_k(key_attn_simt_kernel<T>, a.n_ctas, KS_THREADS, smem, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(key_join_kernel<T>, dim3(a.n_ctas, 8), 256, 0, s, a, KS_T, KS_T / a.G, KS_T);
+}
+}  // namespace
+
+int key_attn_ctas(int dtype, int D, int G, int num_sms) {
+  (void)dtype;
+  (void)G;
+  return num_sms * (D <= 64 ? 2 : 1);
+}
+
+size_t key_attn_ws_floats(int dtype, int D, int G, int H, int n_ctas, int stack_rows) {
+  (void)dtype;
+  (void)G;
+  return 2 * (size_t)n_ctas * KS_T * (D + 2) + 2 * (size_t)stack_rows * H * (D + 2);
+}
+
+cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s) {
+  return a.dtype == SL_BF16 ? run_simt<bf16>(a, s) : run_simt<float>(a, s);
+}
+
+}  // namespace sl

@@ -1,0 +1,196 @@
+// The attention weight each cached key receives from the active rows:
+//   w_bn = sum_h sum_{j in b} exp(scale q_jh . k_n - lse_jh)
+// with the log partition lse the attention left, so that the weights are those
+// of the attention over its whole key set, accumulated over layers and steps
+// as mass = decay mass_prev + w.  A locked position's K/V stay in the cache
+// for the rest of the decode (Paper-Notes, "permanent locking"); the weight
+// says which of them the active rows still look at.
+//
+// A unit is a tile of keys, its inner tiles the row blocks of every K/V head,
+// so the sum over heads and rows stays in registers; units that a CTA's share
+// cut leave one partial sum per key, joined in CTA order by the second kernel.
+#include <algorithm>
+
+#include "common.cuh"
+#include "keys_common.cuh"
+#include "keys_plan.cuh"
+
+namespace sl {
+
+namespace {
+constexpr int MS_T = 64;
+constexpr int MS_THREADS = 256;
+}  // namespace
+
+// mass = decay mass_prev at every position, before the weights are added
+__device__ __forceinline__ void mass_start(const KeyArgs &a, int i, int n_threads) {
+  const long long n = (long long)a.batch * a.n_ctx;
+  for (long long e = i; e < n; e += n_threads)
+    a.mass[e] = a.decay == 0.f ? 0.f : a.decay * a.mass_prev[e];
+}
+
+// 64 keys against 64 packed rows (qr, g) at a time in fp32 arithmetic; thread
+// (ty, tx) of 16 x 16 holds the scores of rows 4 ty + i and keys tx + 16 j.
+template <typename T>
+__global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs a) {
+  extern __shared__ float4 ms_smem4[];
+  __shared__ KeyPlan pl;
+  __shared__ float sL[MS_T], red[MS_THREADS / 16][MS_T];
+  float *smem = reinterpret_cast<float *>(ms_smem4);
+  const int D = a.D, ld = D + 4, d4 = D >> 2;
+  float *sq = smem, *sk = sq + MS_T * ld;
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, lane = tid & 31;
+  const int QR = MS_T / a.G;
+  pdl_wait();
+  if (tid < 32) key_plan_build(pl, a, QR, MS_T, gridDim.x, true, lane);
+  mass_start(a, blockIdx.x * MS_THREADS + tid, gridDim.x * MS_THREADS);
+  __syncthreads();
+  pdl_trigger();
+  const float c2 = a.scale * KEY_LOG2E;
+  int w = min((long long)blockIdx.x * pl.chunk, (long long)pl.wbase[pl.njobs]), job = 0;
+  const int w_end = min((long long)w + pl.chunk, (long long)pl.wbase[pl.njobs]);
+  KeyPiece pc;
+  while (key_next(pl, 1, w, w_end, job, pc)) {
+    const int b = pc.job;
+    const int i0 = pc.unit * MS_T, nv = min(MS_T, pl.kl[b] - i0);
+    const int qn = pl.q0[b + 1] - pl.q0[b], nqt = kp_tiles(qn, QR);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    int hk_staged = -1;
+    for (int t = pc.t0; t < pc.t1; ++t) {
+      const int hk = t / nqt, r0 = pl.q0[b] + (t - hk * nqt) * QR;
+      const int rn = min(QR, pl.q0[b + 1] - r0) * a.G;
+      __syncthreads();
+      if (hk != hk_staged) {
+        hk_staged = hk;
+        for (int i = tid; i < MS_T * d4; i += MS_THREADS) {
+          const int r = i / d4, c = (i - r * d4) * 4;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (r < nv) {
+            const int pos = key_pos(a, b, i0 + r);
+            if (pos >= 0)
+              v = load4((const T *)a.k + ((long long)b * a.n_ctx + pos) * a.ld_kv + hk * D + c);
+          }
+          *reinterpret_cast<float4 *>(sk + r * ld + c) = v;
+        }
+      }
+      for (int i = tid; i < MS_T * d4; i += MS_THREADS) {
+        const int r = i / d4, c = (i - r * d4) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rn) v = load4((const T *)a.q + (r0 + r / a.G) * a.ld_q + (hk * a.G + r % a.G) * D + c);
+        *reinterpret_cast<float4 *>(sq + r * ld + c) = v;
+      }
+      if (tid < MS_T) {
+        // rows that are not there, or saw no key, weigh nothing
+        float L = INFINITY;
+        if (tid < rn) {
+          L = a.lse[(size_t)(r0 + tid / a.G) * a.H + hk * a.G + tid % a.G] * KEY_LOG2E;
+          if (L == -INFINITY) L = INFINITY;
+        }
+        sL[tid] = L;
+      }
+      __syncthreads();
+      float s[4][4] = {};
+      for (int c = 0; c < D; c += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sq + (4 * ty + i) * ld + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * ld + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            s[i][j] = fmaf(x[i].x, y[j].x, s[i][j]);
+            s[i][j] = fmaf(x[i].y, y[j].y, s[i][j]);
+            s[i][j] = fmaf(x[i].z, y[j].z, s[i][j]);
+            s[i][j] = fmaf(x[i].w, y[j].w, s[i][j]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float L = sL[4 * ty + i];
+          // a select, not a product: the score may be NaN where L is +inf
+          acc[j] += L == INFINITY ? 0.f : exp2f(fmaf(s[i][j], c2, -L));
+        }
+    }
+    // the key's sum over the 16 row groups
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) red[ty][tx + 16 * j] = acc[j];
+    __syncthreads();
+    if (tid < nv) {
+      float v = 0.f;
+#pragma unroll
+      for (int y = 0; y < MS_THREADS / 16; ++y) v += red[y][tid];
+      const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
+      float *dst = whole ? a.ws + 2 * (size_t)gridDim.x * MS_T + (size_t)b * a.n_ctx + i0
+                         : a.ws + (size_t)kp_slot(blockIdx.x, pc.t0) * MS_T;
+      dst[tid] = v;
+    }
+  }
+}
+
+// Adds each key's weight: one thread per entry of a key set.  An entry that a
+// list names twice counts twice, so the additions are atomic; otherwise each
+// position receives one addition and the result does not depend on any order.
+__global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int uq, int kt) {
+  __shared__ KeyPlan pl;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x < 32) key_plan_build(pl, a, uq, kt, a.n_ctas, true, threadIdx.x);
+  __syncthreads();
+  const int b = blockIdx.y;
+  const int T = pl.T[b];
+  if (T == 0) return;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < pl.kl[b]; i += gridDim.x * 256) {
+    const int wu = pl.wbase[b] + i / kt * (T + KP_OV);
+    const int c1 = (wu + T + KP_OV - 1) / pl.chunk;
+    float v = 0.f;
+    for (int c = wu / pl.chunk; c <= c1; ++c) {
+      int t0, t1;
+      kp_piece_of(pl, wu, T, c, t0, t1);
+      if (t1 <= t0) continue;
+      v += t0 == 0 && t1 == T
+               ? __ldcg(a.ws + 2 * (size_t)a.n_ctas * kt + (size_t)b * a.n_ctx + i)
+               : __ldcg(a.ws + (size_t)kp_slot(c, t0) * kt + i % kt);
+    }
+    const int pos = key_pos(a, b, i);
+    if (pos >= 0) atomicAdd(a.mass + (size_t)b * a.n_ctx + pos, v);
+  }
+}
+
+// ---------------------------------------------------------------------- host --
+namespace {
+template <typename T> cudaError_t run_mass_simt(const KeyArgs &a, cudaStream_t s) {
+  const size_t smem = (size_t)2 * MS_T * (a.D + 4) * 4;
+  cudaError_t e = cudaFuncSetAttribute(key_mass_simt_kernel<T>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  e = launch_k(key_mass_simt_kernel<T>, a.n_ctas, MS_THREADS, smem, s, a);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(std::min((a.n_ctx + 255) / 256, 256), a.batch);
+  return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, MS_T / a.G, MS_T);
+}
+}  // namespace
+
+int key_mass_ctas(int dtype, int D, int G, int num_sms) {
+  (void)dtype;
+  (void)D;
+  (void)G;
+  return num_sms * 2;
+}
+
+size_t key_mass_ws_floats(int dtype, int D, int G, int batch, int n_ctx, int n_ctas) {
+  (void)dtype;
+  (void)D;
+  (void)G;
+  return 2 * (size_t)n_ctas * MS_T + (size_t)batch * n_ctx;
+}
+
+cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s) {
+  return a.dtype == SL_BF16 ? run_mass_simt<bf16>(a, s) : run_mass_simt<float>(a, s);
+}
+
+}  // namespace sl

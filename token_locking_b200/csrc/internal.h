@@ -15,6 +15,7 @@ namespace sl {
 sl_status fail(sl_status st, const char *fmt, ...);
 sl_status cuda_fail(cudaError_t e, const char *what);
 int *device_error_word();   // per-device int, allocated on first use; nullptr on failure
+unsigned long long wait_limit_ns();   // sl_debug_set_wait_limit (0: the default)
 void note_launch(int n = 1); // count kernels launched by this library
 long long launches_total();
 
@@ -198,6 +199,44 @@ struct TcGemmArgs {
   int swap;
 };
 cudaError_t launch_gemm_tc(const TcGemmArgs &a, int num_sms, int *err, cudaStream_t s);
+
+// ------------------------------------------------- attn_keys.cu, attn_mass.cu
+// Attention over a key set per sequence, and the attention weight each key
+// receives (see keys_plan.cuh for how the work is shared out).
+constexpr int KP_OV = 2;          // a unit's start-up and epilogue, in tile times
+constexpr int KP_MIN_CHUNK = 4;   // least share of a CTA, in tile times
+constexpr int KP_JOIN_NUM = 1, KP_JOIN_DEN = 16;   // joining one packed row, in tile times
+struct KeyArgs {
+  int dtype, batch, n_ctx, M, H, Hkv, G, D;   // G = H / Hkv query heads per K/V head
+  int prefix_len;
+  int stack;                      // the prefix may be a job of its own (ws has room)
+  float scale;
+  const void *q, *k, *v, *kp, *vp;
+  long long ld_q, ld_kv, ld_p, ld_o;
+  const int32_t *seq_off, *key_len, *keys;
+  void *o;
+  float *lse;                     // attention: written (may be null); weight: read
+  const float *mass_prev;
+  float *mass, decay;
+  float *ws;                      // key_ws_floats(...)
+  int n_ctas;                     // CTAs of the launch (attention / weight)
+  int *err;
+  unsigned long long wait_ns;
+};
+// Most CTAs a launch of this head layout uses, and the workspace for it.
+int key_attn_ctas(int dtype, int D, int G, int num_sms);
+int key_mass_ctas(int dtype, int D, int G, int num_sms);
+// [2 nC slots][rows][D + 2] partial rows, then (stacked) [2][rows][H][D + 2].
+size_t key_attn_ws_floats(int dtype, int D, int G, int H, int n_ctas, int stack_rows);
+size_t key_mass_ws_floats(int dtype, int D, int G, int batch, int n_ctx, int n_ctas);
+cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s);
+cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s);
+
+// ------------------------------------------------------------------- evict.cu
+int evict_max_ctx();
+cudaError_t launch_evict(int batch, int n_ctx, int budget, const float *mass,
+                         const uint8_t *protect, const uint8_t *present, int32_t *keys,
+                         int32_t *key_len, uint8_t *present_out, cudaStream_t s);
 
 // ------------------------------------------------------------------ lock.cu
 struct LockStatsArgs {

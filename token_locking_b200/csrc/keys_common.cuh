@@ -1,0 +1,38 @@
+// Helpers shared by the key-set kernels.
+#pragma once
+#include "common.cuh"
+#include "internal.h"
+
+namespace sl {
+
+constexpr float KEY_LOG2E = 1.4426950408889634f;
+constexpr float KEY_LN2 = 0.6931471805599453f;
+
+// 4 consecutive elements as fp32, and back
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const bf16 *p) {
+  const uint2 u = *reinterpret_cast<const uint2 *>(p);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void store4(bf16 *p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 u;
+  u.x = *reinterpret_cast<uint32_t *>(&a);
+  u.y = *reinterpret_cast<uint32_t *>(&b);
+  *reinterpret_cast<uint2 *>(p) = u;
+}
+
+// Position of entry i of sequence b's key set; -1 for a list entry outside
+// [0, n_ctx), which stands for a key and value of zeros and is reported.
+__device__ __forceinline__ int key_pos(const KeyArgs &a, int b, int i) {
+  if (!a.keys) return i;
+  const int n = a.keys[(size_t)b * a.n_ctx + i];
+  if ((unsigned)n < (unsigned)a.n_ctx) return n;
+  atomicExch(a.err, DEV_BAD_INDEX);
+  return -1;
+}
+
+}  // namespace sl

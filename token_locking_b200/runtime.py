@@ -437,3 +437,149 @@ class Sampler:
             self.close()
         except Exception:
             pass
+
+
+def _rows_ptr(t: torch.Tensor, name: str, device, dtype, n_rows=None):
+    """(pointer, row stride) of a 2-D operand with unit column stride."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if n_rows is not None and t.shape[0] != n_rows:
+        raise ValueError(f"{name} has {t.shape[0]} rows, expected {n_rows}")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _dense_ptr(t: Optional[torch.Tensor], name: str, device, dtype, shape):
+    """Pointer of a contiguous tensor of the given shape (None stays None)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+class KeyAttention:
+    """Attention over a key set per sequence and the weight each key receives
+    (sl_key_attn).  Rows of sequence b (seq_off[b] .. seq_off[b + 1]) attend to
+    the cache entries keys[b, :key_len[b]] (or the first key_len[b] entries) and
+    to a prefix shared by the batch.  Owns its workspace on the current device;
+    one call at a time."""
+
+    def __init__(self, batch: int, n_ctx: int, max_rows: int, n_heads: int, head_dim: int,
+                 n_kv_heads: Optional[int] = None, dtype="bf16", prefix: bool = False,
+                 scale: float = 0.0):
+        self.batch, self.n_ctx, self.max_rows = batch, n_ctx, max_rows
+        self.n_heads, self.head_dim = n_heads, head_dim
+        self.n_kv_heads = n_heads if n_kv_heads is None else n_kv_heads
+        self.dtype = _dtype_code(dtype)
+        self.torch_dtype = _TORCH_DT[self.dtype]
+        cfg = A.KeyAttnConfig(self.dtype, batch, n_ctx, max_rows, n_heads, self.n_kv_heads,
+                              head_dim, 1 if prefix else 0, scale)
+        h = C.c_void_p()
+        A.check(A.lib().sl_key_attn_create(C.byref(cfg), C.byref(h)), "sl_key_attn_create")
+        self.handle = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
+
+    def _set(self, seq_off, key_len, keys):
+        B = self.batch
+        return A.KeySet(_dense_ptr(seq_off, "seq_off", self.device, torch.int32, (B + 1,)),
+                        _dense_ptr(key_len, "key_len", self.device, torch.int32, (B,)),
+                        _dense_ptr(keys, "keys", self.device, torch.int32, (B, self.n_ctx)))
+
+    def _width(self, t, name, heads):
+        if t.shape[1] != heads * self.head_dim:
+            raise ValueError(f"{name} has {t.shape[1]} columns, expected {heads * self.head_dim}")
+
+    def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+               seq_off: torch.Tensor, key_len: Optional[torch.Tensor] = None,
+               keys: Optional[torch.Tensor] = None, k_prefix: Optional[torch.Tensor] = None,
+               v_prefix: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+               stream=None):
+        """o [rows, n_heads * head_dim] (and lse [rows, n_heads] fp32) of q over
+        k, v [batch * n_ctx, n_kv_heads * head_dim] and the prefix [P, same]."""
+        dev, dt, rows = self.device, self.torch_dtype, q.shape[0]
+        pq, lq = _rows_ptr(q, "q", dev, dt)
+        pk, lk = _rows_ptr(k, "k", dev, dt, self.batch * self.n_ctx)
+        pv, lv = _rows_ptr(v, "v", dev, dt, self.batch * self.n_ctx)
+        po, lo = _rows_ptr(o, "o", dev, dt, rows)
+        for t, name, heads in ((q, "q", self.n_heads), (k, "k", self.n_kv_heads),
+                               (v, "v", self.n_kv_heads), (o, "o", self.n_heads)):
+            self._width(t, name, heads)
+        if lk != lv:
+            raise ValueError("k and v must have the same row stride")
+        if (k_prefix is None) != (v_prefix is None):
+            raise ValueError("a prefix needs both k_prefix and v_prefix")
+        pkp = pvp = None
+        lp = n_prefix = 0
+        if k_prefix is not None and k_prefix.shape[0] > 0:
+            n_prefix = k_prefix.shape[0]
+            pkp, lp = _rows_ptr(k_prefix, "k_prefix", dev, dt)
+            pvp, lvp = _rows_ptr(v_prefix, "v_prefix", dev, dt, n_prefix)
+            self._width(k_prefix, "k_prefix", self.n_kv_heads)
+            self._width(v_prefix, "v_prefix", self.n_kv_heads)
+            if lp != lvp:
+                raise ValueError("k_prefix and v_prefix must have the same row stride")
+        ks = self._set(seq_off, key_len, keys)
+        pl = _dense_ptr(lse, "lse", dev, torch.float32, (rows, self.n_heads))
+        with torch.cuda.device(dev):
+            A.check(A.lib().sl_key_attention(self.handle, rows, pq, lq, pk, pv, lk, C.byref(ks),
+                                             pkp, pvp, lp, n_prefix, po, lo, pl,
+                                             _stream(stream)), "sl_key_attention")
+
+    def mass(self, q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, mass: torch.Tensor,
+             seq_off: torch.Tensor, key_len: Optional[torch.Tensor] = None,
+             keys: Optional[torch.Tensor] = None, mass_prev: Optional[torch.Tensor] = None,
+             decay: float = 0.0, stream=None):
+        """mass [batch, n_ctx] = decay * mass_prev + the attention weight each key
+        of the sets receives from the rows of q, given their lse."""
+        dev, rows = self.device, q.shape[0]
+        pq, lq = _rows_ptr(q, "q", dev, self.torch_dtype)
+        pk, lk = _rows_ptr(k, "k", dev, self.torch_dtype, self.batch * self.n_ctx)
+        self._width(q, "q", self.n_heads)
+        self._width(k, "k", self.n_kv_heads)
+        ks = self._set(seq_off, key_len, keys)
+        shape = (self.batch, self.n_ctx)
+        pl = _dense_ptr(lse, "lse", dev, torch.float32, (rows, self.n_heads))
+        pp = _dense_ptr(mass_prev, "mass_prev", dev, torch.float32, shape)
+        pm = _dense_ptr(mass, "mass", dev, torch.float32, shape)
+        with torch.cuda.device(dev):
+            A.check(A.lib().sl_key_mass(self.handle, rows, pq, lq, pk, lk, C.byref(ks), pl, decay,
+                                        pp, pm, _stream(stream)), "sl_key_mass")
+
+    def close(self):
+        if getattr(self, "handle", None):
+            A.lib().sl_key_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def kv_evict(mass: torch.Tensor, budget: int, keys: torch.Tensor, key_len: torch.Tensor,
+             protect: Optional[torch.Tensor] = None, present: Optional[torch.Tensor] = None,
+             present_out: Optional[torch.Tensor] = None, stream=None):
+    """Keep the protected entries and the heaviest others up to `budget` per
+    sequence (sl_kv_evict): ascending kept positions into keys [batch, n_ctx],
+    their number into key_len [batch], flags into present_out."""
+    dev = mass.device
+    if not mass.is_cuda or mass.dim() != 2:
+        raise ValueError("mass must be a CUDA tensor [batch, n_ctx]")
+    B, N = mass.shape
+    args = [_dense_ptr(mass, "mass", dev, torch.float32, (B, N)),
+            _dense_ptr(protect, "protect", dev, torch.uint8, (B, N)),
+            _dense_ptr(present, "present", dev, torch.uint8, (B, N)),
+            _dense_ptr(keys, "keys", dev, torch.int32, (B, N)),
+            _dense_ptr(key_len, "key_len", dev, torch.int32, (B,)),
+            _dense_ptr(present_out, "present_out", dev, torch.uint8, (B, N))]
+    with torch.cuda.device(dev):
+        A.check(A.lib().sl_kv_evict(B, N, int(budget), *args, _stream(stream)), "sl_kv_evict")
