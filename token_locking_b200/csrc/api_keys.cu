@@ -77,7 +77,7 @@ sl_status fill_args(const sl_key_attn *a, const char *fn, int rows, const void *
   x->keys = set->d_keys;
   x->ws = a->ws;
   x->err = a->err;
-  x->wait_ns = wait_limit_ns();
+  x->wait_ns = wait_limit_ns() ? wait_limit_ns() : WAIT_LIMIT_NS;
   return SL_OK;
 }
 }  // namespace
@@ -115,19 +115,20 @@ extern "C" sl_status sl_key_attn_create(const sl_key_attn_config *cfg, sl_key_at
   cudaError_t e = cudaGetDevice(&a->device);
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&a->num_sms, cudaDevAttrMultiProcessorCount, a->device);
+  if (e == cudaSuccess) e = key_attn_setup(cfg->dtype, cfg->head_dim);
+  if (e == cudaSuccess) e = key_mass_setup(cfg->dtype, cfg->head_dim);
   if (e != cudaSuccess) {
     delete a;
     return cuda_fail(e, "sl_key_attn_create");
   }
-  a->attn_ctas = key_attn_ctas(cfg->dtype, cfg->head_dim, group, a->num_sms);
+  a->attn_ctas = key_attn_ctas(cfg->dtype, cfg->head_dim, a->num_sms);
   a->mass_ctas = key_mass_ctas(cfg->dtype, cfg->head_dim, group, a->num_sms);
   // a joint pass over the prefix pays while a sequence's rows leave most of a
   // 128-row tile empty; above that the workspace for it is not reserved
   a->stack_rows =
       cfg->prefix ? (int)std::min<long long>(cfg->max_rows, (long long)96 * cfg->batch / group) : 0;
   const size_t floats = std::max(
-      key_attn_ws_floats(cfg->dtype, cfg->head_dim, group, cfg->n_heads, a->attn_ctas,
-                         a->stack_rows),
+      key_attn_ws_floats(cfg->dtype, cfg->head_dim, cfg->n_heads, a->attn_ctas, a->stack_rows),
       key_mass_ws_floats(cfg->dtype, cfg->head_dim, group, cfg->batch, cfg->n_ctx, a->mass_ctas));
   a->err = device_error_word();
   if (!a->err || cudaMalloc((void **)&a->ws, floats * sizeof(float)) != cudaSuccess) {

@@ -335,29 +335,39 @@ namespace {
 size_t simt_smem(int D) { return ((size_t)3 * KS_T * (D + 4) + KS_T * (KS_T + 4)) * 4; }
 
 template <typename T> cudaError_t run_simt(const KeyArgs &a, cudaStream_t s) {
-  const size_t smem = simt_smem(a.D);
-  cudaError_t e = cudaFuncSetAttribute(key_attn_simt_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e =
+      launch_k(key_attn_simt_kernel<T>, a.n_ctas, KS_THREADS, simt_smem(a.D), s, a);
   if (e != cudaSuccess) return e;
-  e = launch_k(key_attn_simt_kernel<T>, a.n_ctas, KS_THREADS, smem, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_k(key_join_kernel<T>, dim3(a.n_ctas, 8), 256, 0, s, a, KS_T, KS_T / a.G, KS_T);
+  return launch_key_join(a, KS_T, KS_T / a.G, KS_T, s);
 }
 }  // namespace
 
-int key_attn_ctas(int dtype, int D, int G, int num_sms) {
-  (void)dtype;
-  (void)G;
+cudaError_t key_attn_setup(int dtype, int D) {
+  if (key_attn_tc_takes(dtype, D)) return key_attn_tc_setup(D);
+  const int smem = (int)simt_smem(D);
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  return dtype == SL_BF16 ? cudaFuncSetAttribute(key_attn_simt_kernel<bf16>, attr, smem)
+                          : cudaFuncSetAttribute(key_attn_simt_kernel<float>, attr, smem);
+}
+
+int key_attn_ctas(int dtype, int D, int num_sms) {
+  if (key_attn_tc_takes(dtype, D)) return num_sms;
   return num_sms * (D <= 64 ? 2 : 1);
 }
 
-size_t key_attn_ws_floats(int dtype, int D, int G, int H, int n_ctas, int stack_rows) {
-  (void)dtype;
-  (void)G;
-  return 2 * (size_t)n_ctas * KS_T * (D + 2) + 2 * (size_t)stack_rows * H * (D + 2);
+size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows) {
+  const size_t slot_rows = key_attn_tc_takes(dtype, D) ? 256 : KS_T;
+  return 2 * (size_t)n_ctas * slot_rows * (D + 2) + 2 * (size_t)stack_rows * H * (D + 2);
+}
+
+cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, int kt, cudaStream_t s) {
+  const dim3 grid(a.n_ctas, 8);
+  return a.dtype == SL_BF16 ? launch_k(key_join_kernel<bf16>, grid, 256, 0, s, a, rt, uq, kt)
+                            : launch_k(key_join_kernel<float>, grid, 256, 0, s, a, rt, uq, kt);
 }
 
 cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s) {
+  if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_attn_tc(a, s);
   return a.dtype == SL_BF16 ? run_simt<bf16>(a, s) : run_simt<float>(a, s);
 }
 

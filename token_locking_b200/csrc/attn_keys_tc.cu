@@ -1,0 +1,502 @@
+// Attention over a key set per sequence (see attn_keys.cu for the operator) on
+// the 5th-generation tensor cores, for bf16 heads of 64 and 128.
+//
+// A unit is two tiles of 128 packed rows (query row, head of the group) of one
+// K/V head against a list of tiles of BN keys; a CTA takes an equal share of
+// all units' tiles (keys_plan.cuh) and runs through its pieces without a break:
+//   warp 0       TMA producer.  Q tiles as boxes [QR query rows][G heads][64],
+//                so that packed rows land in order whatever G; K and V tiles
+//                through a ring of ST slots.  A full tile of the prefix or of a
+//                cache that is not listed is two boxes; listed keys, and the
+//                tile a key set ends in, are gathered four rows at a time, with
+//                a row past the operand (zeros) for entries that are not there:
+//                what lies behind a key set never reaches shared memory.
+//   warp 1       owns TMEM; one lane issues S_j = Q_j K^T and O_j += P_j V
+//   warps 2..9   a softmax warpgroup per row tile j, one row per thread: the
+//                running maximum and sum need no shuffles.  The maximum is
+//                raised only when a tile exceeds it by 2^8 (O is rescaled then);
+//                p is rounded to bf16 for the product (half a step, 2^-9
+//                relative on average), its sum is taken in fp32 before that.
+// The two row tiles are two independent chains (scores, softmax, P V) that
+// share K and V, so that the tensor cores work on one while the other's
+// exponentials are taken.
+#include <string.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "keys_common.cuh"
+#include "keys_plan.cuh"
+#include "tc_ptx.cuh"
+
+namespace sl {
+
+namespace {
+constexpr int KC_ROWS = 128;                  // packed rows of a tile (TMEM lanes)
+constexpr int KC_THREADS = 64 + 2 * 128;
+constexpr float KC_RESCALE = 8.f;
+
+template <int D, int BN> struct KcCfg {
+  static constexpr int NB = D / 64;                     // 128-byte boxes of a row
+  static constexpr int QBOX = KC_ROWS * 128, KBOX = BN * 128;
+  static constexpr int SLOT = NB * KBOX;                // a K or V tile
+  static constexpr int KV_OFF = 2 * NB * QBOX;
+  static constexpr int TAIL = 2048;                     // barriers and plan
+  static constexpr int ST = (232448 - 1024 - TAIL - KV_OFF) / SLOT;
+  static constexpr int BAR_OFF = KV_OFF + ST * SLOT;
+  static constexpr int SMEM = BAR_OFF + TAIL + 1024;    // + alignment
+  static constexpr int B_QF = 0, B_QE = 1, B_F = 2, B_E = 2 + ST, B_TILE = 2 + 2 * ST;
+  static constexpr int B_DRAIN = B_TILE + 8, B_COUNT = B_DRAIN + 1;
+  static constexpr int PLAN_OFF = BAR_OFF + 512;
+  // TMEM columns: per row tile S, then P (two bf16 keys a column), from a
+  // multiple of 64; then O of both
+  static constexpr uint32_t T_COLS = (BN + BN / 2 + 63) / 64 * 64;
+  static constexpr uint32_t O_COL = 2 * T_COLS;
+  static_assert(O_COL + 2 * D <= 512, "TMEM columns");
+  static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
+  static_assert(SMEM <= 232448 && BN % 16 == 0, "shared memory, key tile");
+};
+}  // namespace
+
+struct KcParams {
+  CUtensorMap q, k, v, kg, vg, kp, vp;   // kg, vg: one-row boxes for gathers
+  KeyArgs a;
+};
+
+// N fp32 columns of this thread's TMEM lane (N a multiple of 16), one wait.
+template <int N> __device__ __forceinline__ void tmem_ld_cols(uint32_t t, float *s) {
+#pragma unroll
+  for (int c = 0; c + 32 <= N; c += 32) tmem_ld32_nw(t + c, s + c);
+  if constexpr (N % 32 == 16) tmem_ld16_nw(t + N - 16, s + N - 16);
+  tmem_wait_ld();
+}
+
+__device__ __forceinline__ uint32_t kc_pack(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+
+__device__ __forceinline__ bool kc_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                        unsigned long long lim) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, lim));
+}
+
+template <int D, int BN>
+__global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
+    const __grid_constant__ KcParams p) {
+  using C = KcCfg<D, BN>;
+  extern __shared__ uint8_t kc_smem[];
+  uint8_t *smem = (uint8_t *)(((uintptr_t)kc_smem + 1023) & ~(uintptr_t)1023);
+  const uint32_t sbase = s_addr(smem);
+  const uint32_t bar0 = sbase + C::BAR_OFF;
+  auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  // per row tile: 0 scores ready, 1 scores read, 2 P written, 3 P V done
+  auto tbar = [&](int j, int k) { return bar0 + 8u * (uint32_t)(C::B_TILE + 4 * j + k); };
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::B_COUNT);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  KeyPlan &pl = *reinterpret_cast<KeyPlan *>(smem + C::PLAN_OFF);
+  const KeyArgs &a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const unsigned long long lim = a.wait_ns;
+  const int QR = KC_ROWS / a.G;               // query rows of a tile
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(C::B_QF), 1);
+    mbar_init(bar(C::B_QE), 1);
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(bar(C::B_F + s), 1);
+      mbar_init(bar(C::B_E + s), 1);
+    }
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(tbar(j, 0), 1);               // MMA commit
+      mbar_init(tbar(j, 1), 4);               // the tile's four softmax warps
+      mbar_init(tbar(j, 2), 4);
+      mbar_init(tbar(j, 3), 1);
+    }
+    mbar_init(bar(C::B_DRAIN), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&p.q);
+    tma_prefetch_desc(&p.k);
+    tma_prefetch_desc(&p.v);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     s_addr(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  pdl_wait();
+  if (warp == 0) key_plan_build(pl, a, 2 * QR, BN, gridDim.x, false, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem_base = *tmem_slot;
+  const int tp = kp_tiles(a.prefix_len, BN);
+
+  // every role walks the same pieces
+  const int W = pl.wbase[pl.njobs];
+  int w = (int)min((long long)blockIdx.x * pl.chunk, (long long)W), job = 0;
+  const int w_end = (int)min((long long)w + pl.chunk, (long long)W);
+  KeyPiece pc{};
+  // first query row and query rows of a piece's unit; row tiles it fills
+  auto rows_of = [&](int &r0, int &rn) {
+    const int b = kp_seq(pl, pc.job);
+    r0 = (b < 0 ? pl.q0[0] : pl.q0[b]) + pc.unit * 2 * QR;
+    rn = min(2 * QR, (b < 0 ? pl.q0[a.batch] : pl.q0[b + 1]) - r0);
+    return rn > QR ? 2 : 1;
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    const int oob = a.batch * a.n_ctx;        // the first row past the cache: zeros
+    int n = 0, np = 0;                        // K and V tiles, pieces started
+    bool ok = true;
+    while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+      int r0, rn;
+      const int nj = rows_of(r0, rn), b = kp_seq(pl, pc.job);
+      // entry e of this lane's four rows of tile t, as a cache row; -1: not gathered
+      int nxt[4];
+      auto entries = [&](int t) {
+        const bool pre = b < 0 || (!pl.stacked && t < tp);
+        const int i0 = (pre || pl.stacked ? t : t - tp) * BN + 4 * lane;
+        if (pre || 4 * lane >= BN || t >= pc.t1) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          nxt[e] = i0 + e >= pl.kl[b] ? oob
+                   : a.keys           ? a.keys[(size_t)b * a.n_ctx + i0 + e]
+                                      : i0 + e;
+      };
+      entries(pc.t0);
+      if (!kc_wait(bar(C::B_QE), (uint32_t)(np & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+      if (lane == 0) {
+        mbar_expect_tx(bar(C::B_QF), (uint32_t)(nj * C::NB * 128 * a.G * QR));
+        for (int j = 0; j < nj; ++j)
+          for (int c = 0; c < C::NB; ++c)
+            tma_load_3d(sbase + (j * C::NB + c) * C::QBOX, &p.q, 64 * c, pc.hk * a.G, r0 + j * QR,
+                        bar(C::B_QF));
+      }
+      ++np;
+      for (int t = pc.t0; t < pc.t1; ++t) {
+        const bool pre = b < 0 || (!pl.stacked && t < tp);
+        const int i0 = (pre || pl.stacked ? t : t - tp) * BN;
+        const bool gather = !pre && (a.keys || i0 + BN > pl.kl[b]);
+        int row[4];
+        if (gather) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            int x = nxt[e];
+            if (4 * lane < BN && i0 + 4 * lane + e < pl.kl[b]) {
+              if ((unsigned)x < (unsigned)a.n_ctx) {
+                x += b * a.n_ctx;
+              } else {
+                x = oob;
+                atomicExch(a.err, DEV_BAD_INDEX);
+              }
+            }
+            row[e] = x;
+          }
+        }
+        entries(t + 1);
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int s = n % C::ST;
+          if (!kc_wait(bar(C::B_E + s), (uint32_t)((n / C::ST) & 1) ^ 1u, abort_flag, lim)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sbase + C::KV_OFF + s * C::SLOT;
+          if (lane == 0) mbar_expect_tx(bar(C::B_F + s), C::SLOT);
+          __syncwarp();
+          if (gather) {
+            const CUtensorMap *m = kv ? &p.vg : &p.kg;
+            if (4 * lane < BN)
+#pragma unroll
+              for (int c = 0; c < C::NB; ++c)
+                tma_gather4(dst + c * C::KBOX + lane * 512, m, pc.hk * D + 64 * c, row[0], row[1],
+                            row[2], row[3], bar(C::B_F + s));
+          } else if (lane == 0) {
+            const CUtensorMap *m = pre ? (kv ? &p.vp : &p.kp) : (kv ? &p.v : &p.k);
+            const int y = pre ? i0 : b * a.n_ctx + i0;
+#pragma unroll
+            for (int c = 0; c < C::NB; ++c)
+              tma_load_2d(dst + c * C::KBOX, m, pc.hk * D + 64 * c, y, bar(C::B_F + s));
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicExch(a.err, DEV_TIMEOUT_PRODUCER);
+      *abort_flag = 1;
+    }
+    // every issued copy lands before the CTA can exit
+    if (lane == 0) {
+      volatile int never = 0;
+      if (np > 0) mbar_wait(bar(C::B_QF), (uint32_t)(np - 1) & 1u, &never, lim);
+      for (int s = 0; s < C::ST && s < n; ++s) {
+        const int last = s + (n - 1 - s) / C::ST * C::ST;
+        mbar_wait(bar(C::B_F + s), (uint32_t)(last / C::ST) & 1u, &never, lim);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_bf16_f32<BN>();
+      constexpr uint32_t id_o = idesc_bf16_f32_bmn<D>();
+      int n = 0, np = 0;                      // first K/V slot of the piece, pieces
+      uint32_t cs[2] = {0u, 0u}, cv[2] = {0u, 0u};   // scores and P V products issued
+      bool ok = true;
+      auto slot_wait = [&](int i) {
+        return mbar_wait(bar(C::B_F + i % C::ST), (uint32_t)(i / C::ST) & 1u, abort_flag, lim);
+      };
+      auto issue_s = [&](int i, int j) {
+        const uint32_t sq = sbase + j * C::NB * C::QBOX;
+        const uint32_t sk = sbase + C::KV_OFF + (i % C::ST) * C::SLOT;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc_mma(tmem_base + j * C::T_COLS,
+                 smem_desc_sw128(sq + (kk >> 2) * C::QBOX) + 2 * (kk & 3),
+                 smem_desc_sw128(sk + (kk >> 2) * C::KBOX) + 2 * (kk & 3), id_s, kk > 0 ? 1u : 0u);
+        tc_commit(tbar(j, 0));
+        ++cs[j];
+      };
+      auto issue_pv = [&](int i, int j, bool first) {
+        const uint32_t sv = sbase + C::KV_OFF + (i % C::ST) * C::SLOT;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          tc_mma_ts(tmem_base + C::O_COL + j * D, tmem_base + j * C::T_COLS + BN + kk * 8,
+                    smem_desc_sw128_mn(sv + kk * 2048, C::KBOX, 1024), id_o,
+                    (!first || kk > 0) ? 1u : 0u);
+        tc_commit(tbar(j, 3));
+        ++cv[j];
+      };
+      while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+        int r0, rn;
+        const int nj = rows_of(r0, rn);
+        const int nt = pc.t1 - pc.t0;
+        ok = mbar_wait(bar(C::B_QF), (uint32_t)(np & 1), abort_flag, lim);
+        ++np;
+        // scores of tile t are issued one tile ahead of its P V product
+        for (int t = -1; ok && t < nt; ++t) {
+          if (t + 1 < nt) {
+            const int i = n + 2 * (t + 1);
+            ok = slot_wait(i);
+            for (int j = 0; ok && j < nj; ++j) {
+              // the buffer's last scores have been read
+              ok = mbar_wait(tbar(j, 1), (cs[j] & 1u) ^ 1u, abort_flag, lim);
+              if (!ok) break;
+              tc_fence_after();
+              issue_s(i, j);
+            }
+            if (!ok) break;
+            tc_commit(bar(C::B_E + i % C::ST));
+            if (t + 2 == nt) tc_commit(bar(C::B_QE));
+          }
+          if (t < 0) continue;
+          const int i = n + 2 * t + 1;
+          ok = slot_wait(i);
+          for (int j = 0; ok && j < nj; ++j) {
+            ok = mbar_wait(tbar(j, 2), cv[j] & 1u, abort_flag, lim);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(i, j, t == 0);
+          }
+          if (!ok) break;
+          tc_commit(bar(C::B_E + i % C::ST));
+        }
+        n += 2 * nt;
+      }
+      if (!ok) {
+        atomicExch(a.err, DEV_TIMEOUT_MMA);
+        *abort_flag = 1;
+      }
+      tc_commit(bar(C::B_DRAIN));
+      volatile int never = 0;
+      mbar_wait(bar(C::B_DRAIN), 0, &never, lim);
+    }
+  } else {
+    // ---------------------------------------------------------- softmax
+    const int j = (warp - 2) >> 2;            // row tile of this warpgroup
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;        // packed row (TMEM lane)
+    const int rq = r / a.G, rg = r - rq * a.G;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t t_s = tmem_base + lane_off + j * C::T_COLS;
+    const uint32_t t_o = tmem_base + lane_off + C::O_COL + j * D;
+    const uint32_t t_p = t_s + BN;
+    const float c2 = a.scale * KEY_LOG2E;
+    const size_t slot_f = (size_t)2 * QR * a.G * (D + 2);
+    uint32_t cs = 0;                          // score tiles taken
+    bool ok = true;
+    while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+      int r0, rn;
+      if (rows_of(r0, rn) <= j) continue;
+      const int b = kp_seq(pl, pc.job);
+      float m = -INFINITY, l = 0.f;
+      float s[BN];
+      for (int t = pc.t0; t < pc.t1; ++t, ++cs) {
+        const bool pre = b < 0 || (!pl.stacked && t < tp);
+        const int nv = (pre ? a.prefix_len : pl.kl[b]) - (pre || pl.stacked ? t : t - tp) * BN;
+        if (!kc_wait(tbar(j, 0), cs & 1u, abort_flag, lim)) { ok = false; break; }
+        tc_fence_after();
+        tmem_ld_cols<BN>(t_s, s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tbar(j, 1));
+        if (nv < BN) {
+#pragma unroll
+          for (int i = 0; i < BN; ++i) s[i] = i < nv ? s[i] : -INFINITY;
+        }
+        float mx[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx[e] = s[e];
+#pragma unroll
+        for (int i = 8; i < BN; ++i) mx[i & 7] = fmaxf(mx[i & 7], s[i]);
+        const float mt = c2 * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                    fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        const bool first = t == pc.t0;
+        const float m_new = fmaxf(m, mt);
+        const bool resc = !first && m_new > m + KC_RESCALE;
+        const float m_use = (first || resc) ? m_new : m;
+        const float alpha = resc ? (m == -INFINITY ? 0.f : ex2_approx(m - m_new)) : 1.f;
+        const float m_sub = m_use == -INFINITY ? 0.f : m_use;   // all scores -inf: p = 0
+        float sm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < BN; ++i) {
+          s[i] = ex2_approx(fmaf(s[i], c2, -m_sub));
+          sm[i & 7] += s[i];
+        }
+        const float rs = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+        // the last P V product has read P and written O
+        if (!first && !kc_wait(tbar(j, 3), (cs & 1u) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        tc_fence_after();
+        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32_nw(t_o + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(t_o + c, o);
+          }
+        }
+        l = l * alpha + rs;
+        m = m_use;
+        uint32_t pk[BN / 2];
+#pragma unroll
+        for (int e = 0; e < BN / 2; ++e) pk[e] = kc_pack(s[2 * e], s[2 * e + 1]);
+#pragma unroll
+        for (int c = 0; c + 32 <= BN / 2; c += 32) tmem_st32_u(t_p + c, pk + c);
+        if constexpr (BN / 2 % 32 == 8) tmem_st8_u(t_p + BN / 2 - 8, pk + BN / 2 - 8);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tbar(j, 2));
+      }
+      if (!ok) break;
+      if (!kc_wait(tbar(j, 3), (cs - 1u) & 1u, abort_flag, lim)) { ok = false; break; }
+      tc_fence_after();
+      // O leaves in 64-column parts: final rows of a whole unit, else partial ones
+      const bool live = rq < QR && j * QR + rq < rn;
+      const int row = r0 + j * QR + rq, h = pc.hk * a.G + rg;
+      const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
+      if (whole && !pl.stacked) {
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        bf16 *orow = (bf16 *)a.o + row * a.ld_o + h * D;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          tmem_ld_cols<64>(t_o + c0, s);
+          if (live) {
+            uint4 *dst = reinterpret_cast<uint4 *>(orow + c0);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              dst[c] = make_uint4(kc_pack(s[8 * c] * inv, s[8 * c + 1] * inv),
+                                  kc_pack(s[8 * c + 2] * inv, s[8 * c + 3] * inv),
+                                  kc_pack(s[8 * c + 4] * inv, s[8 * c + 5] * inv),
+                                  kc_pack(s[8 * c + 6] * inv, s[8 * c + 7] * inv));
+          }
+        }
+        if (live && a.lse)
+          a.lse[(size_t)row * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * KEY_LN2;
+      } else {
+        float *rec = whole ? a.ws + 2 * (size_t)gridDim.x * slot_f +
+                                 (((size_t)(b < 0 ? 0 : 1) * a.M + row) * a.H + h) * (D + 2)
+                           : a.ws + kp_slot(blockIdx.x, pc.t0) * slot_f +
+                                 (size_t)(j * QR * a.G + r) * (D + 2);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 64) {
+          tmem_ld_cols<64>(t_o + c0, s);
+          if (live) {
+            float2 *dst = reinterpret_cast<float2 *>(rec + 2 + c0);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) dst[c] = make_float2(s[2 * c], s[2 * c + 1]);
+          }
+        }
+        if (live) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);
+      }
+    }
+    if (!ok && lane == 0) {
+      atomicExch(a.err, DEV_TIMEOUT_EPI);
+      *abort_flag = 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                 "r"(512)
+                 : "memory");
+  }
+}
+
+// ---------------------------------------------------------------------- host --
+namespace {
+template <int D> struct KcBn;                 // key tile: S, P and O of two row tiles fill TMEM
+template <> struct KcBn<128> { static constexpr int v = 80; };
+template <> struct KcBn<64> { static constexpr int v = 128; };
+
+template <int D> cudaError_t run_tc(const KeyArgs &a, cudaStream_t s) {
+  constexpr int BN = KcBn<D>::v;
+  using C = KcCfg<D, BN>;
+  KcParams p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  const int QR = KC_ROWS / a.G;
+  const long long rows = (long long)a.batch * a.n_ctx;
+  bool ok = tma_encode_heads(&p.q, a.q, a.M, a.H, D, a.ld_q, a.G, QR) &&
+            tma_encode_rows(&p.k, a.k, rows, a.Hkv * D, a.ld_kv, BN) &&
+            tma_encode_rows(&p.v, a.v, rows, a.Hkv * D, a.ld_kv, BN) &&
+            tma_encode_rows(&p.kg, a.k, rows, a.Hkv * D, a.ld_kv, 1) &&
+            tma_encode_rows(&p.vg, a.v, rows, a.Hkv * D, a.ld_kv, 1);
+  if (ok && a.prefix_len > 0)
+    ok = tma_encode_rows(&p.kp, a.kp, a.prefix_len, a.Hkv * D, a.ld_p, BN) &&
+         tma_encode_rows(&p.vp, a.vp, a.prefix_len, a.Hkv * D, a.ld_p, BN);
+  if (!ok) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_k(key_attn_tc_kernel<D, BN>, a.n_ctas, KC_THREADS, C::SMEM, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_key_join(a, 2 * QR * a.G, 2 * QR, BN, s);
+}
+}  // namespace
+
+cudaError_t key_attn_tc_setup(int D) {
+  return D == 128 ? cudaFuncSetAttribute(key_attn_tc_kernel<128, KcBn<128>::v>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         KcCfg<128, KcBn<128>::v>::SMEM)
+                  : cudaFuncSetAttribute(key_attn_tc_kernel<64, KcBn<64>::v>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         KcCfg<64, KcBn<64>::v>::SMEM);
+}
+
+bool key_attn_tc_takes(int dtype, int D) { return dtype == SL_BF16 && (D == 64 || D == 128); }
+
+cudaError_t launch_key_attn_tc(const KeyArgs &a, cudaStream_t s) {
+  return a.D == 128 ? run_tc<128>(a, s) : run_tc<64>(a, s);
+}
+
+}  // namespace sl

@@ -163,17 +163,23 @@ __global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int 
 
 // ---------------------------------------------------------------------- host --
 namespace {
+size_t mass_simt_smem(int D) { return (size_t)2 * MS_T * (D + 4) * 4; }
+
 template <typename T> cudaError_t run_mass_simt(const KeyArgs &a, cudaStream_t s) {
-  const size_t smem = (size_t)2 * MS_T * (a.D + 4) * 4;
-  cudaError_t e = cudaFuncSetAttribute(key_mass_simt_kernel<T>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  e = launch_k(key_mass_simt_kernel<T>, a.n_ctas, MS_THREADS, smem, s, a);
+  const cudaError_t e =
+      launch_k(key_mass_simt_kernel<T>, a.n_ctas, MS_THREADS, mass_simt_smem(a.D), s, a);
   if (e != cudaSuccess) return e;
   const dim3 grid(std::min((a.n_ctx + 255) / 256, 256), a.batch);
   return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, MS_T / a.G, MS_T);
 }
 }  // namespace
+
+cudaError_t key_mass_setup(int dtype, int D) {
+  const int smem = (int)mass_simt_smem(D);
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  return dtype == SL_BF16 ? cudaFuncSetAttribute(key_mass_simt_kernel<bf16>, attr, smem)
+                          : cudaFuncSetAttribute(key_mass_simt_kernel<float>, attr, smem);
+}
 
 int key_mass_ctas(int dtype, int D, int G, int num_sms) {
   (void)dtype;

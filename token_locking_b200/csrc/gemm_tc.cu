@@ -56,6 +56,34 @@ bool tma_encode(TmaMat *m, const void *ptr, int rows, int cols, int box_rows) {
   return r == CUDA_SUCCESS;
 }
 
+// [rows][cols] with row stride ld (elements): boxes of 64 columns x box_rows.
+bool tma_encode_rows(CUtensorMap *m, const void *ptr, long long rows, int cols, long long ld,
+                     int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t gstride[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), gdim, gstride, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [rows][heads][d] with row stride ld: boxes of 64 columns x box_heads x box_rows.
+bool tma_encode_heads(CUtensorMap *m, const void *ptr, int rows, int heads, int d, long long ld,
+                      int box_heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t gdim[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t gstride[2] = {(cuuint64_t)d * 2, (cuuint64_t)ld * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), gdim, gstride, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Output descriptor for the TMA epilogue: [rows][cols] with leading dimension
 // ld (elements), 32-row boxes of 128 bytes (32 fp32 or 64 bf16 columns), 128-byte
 // swizzle.  Rows past `rows` are clipped by the copy engine.

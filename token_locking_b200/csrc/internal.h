@@ -156,6 +156,10 @@ struct TmaMat {
   int box_rows;          // rows per TMA box
 };
 bool tma_encode(TmaMat *m, const void *ptr, int rows, int cols, int box_rows);
+bool tma_encode_rows(CUtensorMap *m, const void *ptr, long long rows, int cols, long long ld,
+                     int box_rows);
+bool tma_encode_heads(CUtensorMap *m, const void *ptr, int rows, int heads, int d, long long ld,
+                      int box_heads, int box_rows);
 bool tma_encode_out(TmaMat *m, const void *ptr, int rows, int cols, int ld, bool f32);
 
 struct TcGemmArgs {
@@ -223,14 +227,23 @@ struct KeyArgs {
   int *err;
   unsigned long long wait_ns;
 };
+// Kernel attributes of this head layout on the current device.
+cudaError_t key_attn_setup(int dtype, int D);
+cudaError_t key_mass_setup(int dtype, int D);
+cudaError_t key_attn_tc_setup(int D);
 // Most CTAs a launch of this head layout uses, and the workspace for it.
-int key_attn_ctas(int dtype, int D, int G, int num_sms);
+int key_attn_ctas(int dtype, int D, int num_sms);
 int key_mass_ctas(int dtype, int D, int G, int num_sms);
 // [2 nC slots][rows][D + 2] partial rows, then (stacked) [2][rows][H][D + 2].
-size_t key_attn_ws_floats(int dtype, int D, int G, int H, int n_ctas, int stack_rows);
+size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows);
 size_t key_mass_ws_floats(int dtype, int D, int G, int batch, int n_ctx, int n_ctas);
 cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s);
 cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s);
+// bf16 heads of 64 and 128 on the tensor cores (attn_keys_tc.cu)
+bool key_attn_tc_takes(int dtype, int D);
+cudaError_t launch_key_attn_tc(const KeyArgs &a, cudaStream_t s);
+// Joins partial rows: slots of rt packed rows, units of uq query rows, tiles of kt keys.
+cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, int kt, cudaStream_t s);
 
 // ------------------------------------------------------------------- evict.cu
 int evict_max_ctx();
