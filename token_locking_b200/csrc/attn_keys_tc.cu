@@ -4,15 +4,17 @@
 // A unit is two tiles of 128 packed rows (query row, head of the group) of one
 // K/V head against a list of tiles of BN keys; a CTA takes an equal share of
 // all units' tiles (keys_plan.cuh) and runs through its pieces without a break:
-//   warp 0       TMA producer.  Q tiles as boxes [QR query rows][G heads][64],
-//                so that packed rows land in order whatever G; K and V tiles
-//                through a ring of ST slots.  A full tile of the prefix or of a
-//                cache that is not listed is two boxes; listed keys, and the
-//                tile a key set ends in, are gathered four rows at a time, with
-//                a row past the operand (zeros) for entries that are not there:
-//                what lies behind a key set never reaches shared memory.
+//   warps 0,2,3  producers.  Warp 0 copies Q by TMA in boxes [QR query rows]
+//                [G heads][64], so that packed rows land in order whatever G,
+//                and every full tile of the prefix or of an unlisted cache.
+//                Listed keys, and the tile a key set ends in, are copied row by
+//                row by all three warps (16-byte asynchronous copies, three tiles
+//                in flight), zeros for entries that are not there: what lies
+//                behind a key set never reaches shared memory.  (Four-row TMA
+//                gathers instead took 17 clocks a row of 128 bytes, 7200 clocks
+//                a tile.)
 //   warp 1       owns TMEM; one lane issues S_j = Q_j K^T and O_j += P_j V
-//   warps 2..9   a softmax warpgroup per row tile j, one row per thread: the
+//   warps 4..11  a softmax warpgroup per row tile j, one row per thread: the
 //                running maximum and sum need no shuffles.  The maximum is
 //                raised only when a tile exceeds it by 2^8 (O is rescaled then);
 //                p is rounded to bf16 for the product (half a step, 2^-9
@@ -33,7 +35,7 @@ namespace sl {
 
 namespace {
 constexpr int KC_ROWS = 128;                  // packed rows of a tile (TMEM lanes)
-constexpr int KC_THREADS = 64 + 2 * 128;
+constexpr int KC_THREADS = 128 + 2 * 128;
 constexpr float KC_RESCALE = 8.f;
 
 template <int D, int BN> struct KcCfg {
@@ -42,11 +44,17 @@ template <int D, int BN> struct KcCfg {
   static constexpr int SLOT = NB * KBOX;                // a K or V tile
   static constexpr int KV_OFF = 2 * NB * QBOX;
   static constexpr int TAIL = 2048;                     // barriers and plan
-  static constexpr int ST = (232448 - 1024 - TAIL - KV_OFF) / SLOT;
-  static constexpr int BAR_OFF = KV_OFF + ST * SLOT;
+  // ring of NP stages, a K and a V tile each
+  static constexpr int NP = (232448 - 1024 - TAIL - KV_OFF) / (2 * SLOT);
+  static constexpr int BAR_OFF = KV_OFF + 2 * NP * SLOT;
   static constexpr int SMEM = BAR_OFF + TAIL + 1024;    // + alignment
-  static constexpr int B_QF = 0, B_QE = 1, B_F = 2, B_E = 2 + ST, B_TILE = 2 + 2 * ST;
+  // barriers: Q full, Q free; per stage K full, K free, V full, V free
+  static constexpr int B_QF = 0, B_QE = 1, B_RING = 2, B_TILE = 2 + 4 * NP;
   static constexpr int B_DRAIN = B_TILE + 8, B_COUNT = B_DRAIN + 1;
+  // row copies: 16-byte chunks of a row, rows of a warp instruction, tiles a
+  // warp keeps in flight
+  static constexpr int CH = D / 8, RPI = 32 / CH, LAG = 3;
+  static constexpr int NI = (BN / RPI + 2) / 3;         // instructions of a warp, at most
   static constexpr int PLAN_OFF = BAR_OFF + 512;
   // TMEM columns: per row tile S, then P (two bf16 keys a column), from a
   // multiple of 64; then O of both
@@ -54,12 +62,14 @@ template <int D, int BN> struct KcCfg {
   static constexpr uint32_t O_COL = 2 * T_COLS;
   static_assert(O_COL + 2 * D <= 512, "TMEM columns");
   static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
+  static_assert(NI * RPI <= 32, "a lane per row of a warp's share");
+  static_assert(LAG < NP, "row copies in flight");
   static_assert(SMEM <= 232448 && BN % 16 == 0, "shared memory, key tile");
 };
 }  // namespace
 
 struct KcParams {
-  CUtensorMap q, k, v, kg, vg, kp, vp;   // kg, vg: one-row boxes for gathers
+  CUtensorMap q, k, v, kp, vp;
   KeyArgs a;
 };
 
@@ -81,6 +91,26 @@ __device__ __forceinline__ bool kc_wait(uint32_t bar, uint32_t parity, volatile 
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, lim));
 }
 
+// One lane of the warp (the same every time).
+__device__ __forceinline__ bool kc_elect() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok));
+  return ok != 0;
+}
+// 16 bytes to shared memory, zeros where the source is not there.
+__device__ __forceinline__ void kc_copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void kc_copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void kc_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D, int BN>
 __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     const __grid_constant__ KcParams p) {
@@ -92,21 +122,26 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   // per row tile: 0 scores ready, 1 scores read, 2 P written, 3 P V done
   auto tbar = [&](int j, int k) { return bar0 + 8u * (uint32_t)(C::B_TILE + 4 * j + k); };
+  // stage s: K (0) or V (1), full (0) or free (1)
+  auto rbar = [&](int s, int kv, int e) {
+    return bar0 + 8u * (uint32_t)(C::B_RING + 4 * s + 2 * kv + e);
+  };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::B_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   KeyPlan &pl = *reinterpret_cast<KeyPlan *>(smem + C::PLAN_OFF);
   const KeyArgs &a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const unsigned long long lim = a.wait_ns;
   const int QR = KC_ROWS / a.G;               // query rows of a tile
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::B_QF), 1);
     mbar_init(bar(C::B_QE), 1);
-    for (int s = 0; s < C::ST; ++s) {
-      mbar_init(bar(C::B_F + s), 1);
-      mbar_init(bar(C::B_E + s), 1);
-    }
+    for (int s = 0; s < C::NP; ++s)
+      for (int kv = 0; kv < 2; ++kv) {
+        mbar_init(rbar(s, kv, 0), 3);         // the three producer warps
+        mbar_init(rbar(s, kv, 1), 1);         // MMA commit
+      }
     for (int j = 0; j < 2; ++j) {
       mbar_init(tbar(j, 0), 1);               // MMA commit
       mbar_init(tbar(j, 1), 4);               // the tile's four softmax warps
@@ -149,176 +184,235 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     return rn > QR ? 2 : 1;
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
-    const int oob = a.batch * a.n_ctx;        // the first row past the cache: zeros
-    int n = 0, np = 0;                        // K and V tiles, pieces started
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // --------------------------------------------------------- producers
+    const int pw = warp == 0 ? 0 : warp - 1;  // 0..2
+    const int g0 = lane / C::CH, ch = lane % C::CH;
+    // instruction i of this warp copies rows (3 i + pw) RPI + g0; lane l holds
+    // the cache position of the l-th row of the warp's share
+    const int my_row = (3 * (lane / C::RPI) + pw) * C::RPI + lane % C::RPI;
+    int st = 0, np = 0, n = 0;                // stage, pieces, tiles
+    uint32_t ph = 0;
     bool ok = true;
     while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
       int r0, rn;
       const int nj = rows_of(r0, rn), b = kp_seq(pl, pc.job);
-      // entry e of this lane's four rows of tile t, as a cache row; -1: not gathered
-      int nxt[4];
-      auto entries = [&](int t) {
+      // position of this lane's row in tile t's copy, -1 where there is none
+      auto entry = [&](int t) {
         const bool pre = b < 0 || (!pl.stacked && t < tp);
-        const int i0 = (pre || pl.stacked ? t : t - tp) * BN + 4 * lane;
-        if (pre || 4 * lane >= BN || t >= pc.t1) return;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          nxt[e] = i0 + e >= pl.kl[b] ? oob
-                   : a.keys           ? a.keys[(size_t)b * a.n_ctx + i0 + e]
-                                      : i0 + e;
+        const int i = (pl.stacked ? t : t - tp) * BN + my_row;
+        if (pre || t >= pc.t1 || lane >= C::NI * C::RPI || my_row >= BN || i >= pl.kl[b]) return -1;
+        return key_pos(a, b, i);
       };
-      entries(pc.t0);
-      if (!kc_wait(bar(C::B_QE), (uint32_t)(np & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
-      if (lane == 0) {
-        mbar_expect_tx(bar(C::B_QF), (uint32_t)(nj * C::NB * 128 * a.G * QR));
-        for (int j = 0; j < nj; ++j)
-          for (int c = 0; c < C::NB; ++c)
-            tma_load_3d(sbase + (j * C::NB + c) * C::QBOX, &p.q, 64 * c, pc.hk * a.G, r0 + j * QR,
-                        bar(C::B_QF));
+      int nxt = entry(pc.t0);
+      if (pw == 0) {
+        if (!kc_wait(bar(C::B_QE), (uint32_t)(np & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_expect_tx(bar(C::B_QF), (uint32_t)(nj * C::NB * 128 * a.G * QR));
+          for (int j = 0; j < nj; ++j)
+            for (int c = 0; c < C::NB; ++c)
+              tma_load_3d(sbase + (j * C::NB + c) * C::QBOX, &p.q, 64 * c, pc.hk * a.G,
+                          r0 + j * QR, bar(C::B_QF));
+        }
       }
       ++np;
-      for (int t = pc.t0; t < pc.t1; ++t) {
+      // tiles whose copies this warp has issued but not yet handed over, and
+      // the stage of the first of them
+      int pend = 0, pst = st;
+      auto hand_over = [&]() {
+        fence_proxy_async_smem();             // written by copies, read by the tensor cores
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(rbar(pst, 0, 0));
+          mbar_arrive(rbar(pst, 1, 0));
+        }
+        pst = pst + 1 == C::NP ? 0 : pst + 1;
+        --pend;
+      };
+      for (int t = pc.t0; t < pc.t1; ++t, ++n) {
         const bool pre = b < 0 || (!pl.stacked && t < tp);
         const int i0 = (pre || pl.stacked ? t : t - tp) * BN;
-        const bool gather = !pre && (a.keys || i0 + BN > pl.kl[b]);
-        int row[4];
-        if (gather) {
+        const bool by_row = !pre && (a.keys || i0 + BN > pl.kl[b]);
+        const int pos = nxt;
+        nxt = entry(t + 1);
+        const uint32_t dst = sbase + C::KV_OFF + 2 * st * C::SLOT;
+        if (by_row) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            int x = nxt[e];
-            if (4 * lane < BN && i0 + 4 * lane + e < pl.kl[b]) {
-              if ((unsigned)x < (unsigned)a.n_ctx) {
-                x += b * a.n_ctx;
-              } else {
-                x = oob;
-                atomicExch(a.err, DEV_BAD_INDEX);
-              }
+          for (int kv = 0; kv < 2; ++kv) {
+            if (!kc_wait(rbar(st, kv, 1), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
+            const bf16 *src = (const bf16 *)(kv ? a.v : a.k) + (long long)b * a.n_ctx * a.ld_kv +
+                              pc.hk * D + ch * 8;
+            const uint32_t d0 = dst + kv * C::SLOT + (ch >> 3) * C::KBOX;
+#pragma unroll
+            for (int i = 0; i < C::NI; ++i) {
+              const int ps = __shfl_sync(0xffffffffu, pos, i * C::RPI + g0);
+              const int row = (3 * i + pw) * C::RPI + g0;
+              if (row < BN)
+                kc_copy16(d0 + row * 128 + (((ch ^ row) & 7) << 4),
+                          src + (ps < 0 ? 0 : ps) * a.ld_kv, ps >= 0);
             }
-            row[e] = x;
           }
-        }
-        entries(t + 1);
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int s = n % C::ST;
-          if (!kc_wait(bar(C::B_E + s), (uint32_t)((n / C::ST) & 1) ^ 1u, abort_flag, lim)) {
-            ok = false;
-            break;
+          if (!ok) break;
+          kc_copy_commit();
+          if (++pend == C::LAG) {
+            kc_copy_wait<C::LAG - 1>();
+            hand_over();
           }
-          const uint32_t dst = sbase + C::KV_OFF + s * C::SLOT;
-          if (lane == 0) mbar_expect_tx(bar(C::B_F + s), C::SLOT);
-          __syncwarp();
-          if (gather) {
-            const CUtensorMap *m = kv ? &p.vg : &p.kg;
-            if (4 * lane < BN)
-#pragma unroll
-              for (int c = 0; c < C::NB; ++c)
-                tma_gather4(dst + c * C::KBOX + lane * 512, m, pc.hk * D + 64 * c, row[0], row[1],
-                            row[2], row[3], bar(C::B_F + s));
-          } else if (lane == 0) {
-            const CUtensorMap *m = pre ? (kv ? &p.vp : &p.kp) : (kv ? &p.v : &p.k);
+        } else {
+          if (pend > 0) {
+            kc_copy_wait<0>();
+            while (pend > 0) hand_over();
+          }
+          if (pw == 0) {
             const int y = pre ? i0 : b * a.n_ctx + i0;
 #pragma unroll
-            for (int c = 0; c < C::NB; ++c)
-              tma_load_2d(dst + c * C::KBOX, m, pc.hk * D + 64 * c, y, bar(C::B_F + s));
+            for (int kv = 0; kv < 2; ++kv) {
+              if (!kc_wait(rbar(st, kv, 1), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
+              if (lane == 0) {
+                const CUtensorMap *m = pre ? (kv ? &p.vp : &p.kp) : (kv ? &p.v : &p.k);
+                mbar_expect_tx(rbar(st, kv, 0), C::SLOT);
+#pragma unroll
+                for (int c = 0; c < C::NB; ++c)
+                  tma_load_2d(dst + kv * C::SLOT + c * C::KBOX, m, pc.hk * D + 64 * c, y,
+                              rbar(st, kv, 0));
+              }
+            }
+            if (!ok) break;
+          } else {
+            if (!kc_wait(rbar(st, 0, 1), ph ^ 1u, abort_flag, lim) ||
+                !kc_wait(rbar(st, 1, 1), ph ^ 1u, abort_flag, lim)) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              mbar_arrive(rbar(st, 0, 0));
+              mbar_arrive(rbar(st, 1, 0));
+            }
           }
+          pst = st + 1 == C::NP ? 0 : st + 1;
         }
-        if (!ok) break;
+        if (++st == C::NP) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (pend > 0) {
+        kc_copy_wait<0>();
+        while (pend > 0) hand_over();
       }
     }
+    kc_copy_wait<0>();
     if (!ok && lane == 0) {
       atomicExch(a.err, DEV_TIMEOUT_PRODUCER);
       *abort_flag = 1;
     }
-    // every issued copy lands before the CTA can exit
-    if (lane == 0) {
+    // Every copy lands before the CTA can exit: the MMA warp has waited for each
+    // stage, unless a wait ran out.  Then the stages' last fills are waited for
+    // here; one that not every producer handed over costs its share of the limit.
+    if (pw == 0 && lane == 0 && *abort_flag) {
       volatile int never = 0;
       if (np > 0) mbar_wait(bar(C::B_QF), (uint32_t)(np - 1) & 1u, &never, lim);
-      for (int s = 0; s < C::ST && s < n; ++s) {
-        const int last = s + (n - 1 - s) / C::ST * C::ST;
-        mbar_wait(bar(C::B_F + s), (uint32_t)(last / C::ST) & 1u, &never, lim);
-      }
+      for (int s = 0; s < C::NP; ++s)
+        for (int kv = 0; kv < 2; ++kv)
+          mbar_wait(rbar(s, kv, 0), s <= st ? ph : ph ^ 1u, &never, lim / (2 * C::NP));
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16_f32<BN>();
-      constexpr uint32_t id_o = idesc_bf16_f32_bmn<D>();
-      int n = 0, np = 0;                      // first K/V slot of the piece, pieces
-      uint32_t cs[2] = {0u, 0u}, cv[2] = {0u, 0u};   // scores and P V products issued
-      bool ok = true;
-      auto slot_wait = [&](int i) {
-        return mbar_wait(bar(C::B_F + i % C::ST), (uint32_t)(i / C::ST) & 1u, abort_flag, lim);
-      };
-      auto issue_s = [&](int i, int j) {
-        const uint32_t sq = sbase + j * C::NB * C::QBOX;
-        const uint32_t sk = sbase + C::KV_OFF + (i % C::ST) * C::SLOT;
+    constexpr uint32_t id_s = idesc_bf16_f32<BN>();
+    constexpr uint32_t id_o = idesc_bf16_f32_bmn<D>();
+    const bool leader = kc_elect();
+    const uint64_t dq = smem_desc_sw128(sbase);
+    const uint64_t dk = smem_desc_sw128(sbase + C::KV_OFF);
+    const uint64_t dv = smem_desc_sw128_mn(sbase + C::KV_OFF + C::SLOT, C::KBOX, 1024);
+    int np = 0;
+    int ks = 0, vs = 0;                       // stages of the next scores and P V product
+    uint32_t kph = 0, vph = 0;
+    uint32_t cs[2] = {0u, 0u}, cv[2] = {0u, 0u};   // scores and P V products issued
+    bool ok = true;
+    while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+      int r0, rn;
+      const int nj = rows_of(r0, rn);
+      const int nt = pc.t1 - pc.t0;
+      ok = kc_wait(bar(C::B_QF), (uint32_t)(np & 1), abort_flag, lim);
+      ++np;
+      // scores of tile t are issued one tile ahead of its P V product
+      for (int t = -1; ok && t < nt; ++t) {
+        if (t + 1 < nt) {
+          ok = kc_wait(rbar(ks, 0, 0), kph, abort_flag, lim);
+          if (!ok) break;
+          const uint64_t bk = dk + (uint64_t)(uint32_t)(ks * (2 * C::SLOT >> 4));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc_mma(tmem_base + j * C::T_COLS,
-                 smem_desc_sw128(sq + (kk >> 2) * C::QBOX) + 2 * (kk & 3),
-                 smem_desc_sw128(sk + (kk >> 2) * C::KBOX) + 2 * (kk & 3), id_s, kk > 0 ? 1u : 0u);
-        tc_commit(tbar(j, 0));
-        ++cs[j];
-      };
-      auto issue_pv = [&](int i, int j, bool first) {
-        const uint32_t sv = sbase + C::KV_OFF + (i % C::ST) * C::SLOT;
-#pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          tc_mma_ts(tmem_base + C::O_COL + j * D, tmem_base + j * C::T_COLS + BN + kk * 8,
-                    smem_desc_sw128_mn(sv + kk * 2048, C::KBOX, 1024), id_o,
-                    (!first || kk > 0) ? 1u : 0u);
-        tc_commit(tbar(j, 3));
-        ++cv[j];
-      };
-      while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
-        int r0, rn;
-        const int nj = rows_of(r0, rn);
-        const int nt = pc.t1 - pc.t0;
-        ok = mbar_wait(bar(C::B_QF), (uint32_t)(np & 1), abort_flag, lim);
-        ++np;
-        // scores of tile t are issued one tile ahead of its P V product
-        for (int t = -1; ok && t < nt; ++t) {
-          if (t + 1 < nt) {
-            const int i = n + 2 * (t + 1);
-            ok = slot_wait(i);
-            for (int j = 0; ok && j < nj; ++j) {
-              // the buffer's last scores have been read
-              ok = mbar_wait(tbar(j, 1), (cs[j] & 1u) ^ 1u, abort_flag, lim);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(i, j);
-            }
-            if (!ok) break;
-            tc_commit(bar(C::B_E + i % C::ST));
-            if (t + 2 == nt) tc_commit(bar(C::B_QE));
-          }
-          if (t < 0) continue;
-          const int i = n + 2 * t + 1;
-          ok = slot_wait(i);
-          for (int j = 0; ok && j < nj; ++j) {
-            ok = mbar_wait(tbar(j, 2), cv[j] & 1u, abort_flag, lim);
+          for (int j = 0; j < 2; ++j) {
+            if (j >= nj) break;
+            // the buffer's last scores have been read
+            ok = kc_wait(tbar(j, 1), (cs[j] & 1u) ^ 1u, abort_flag, lim);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(i, j, t == 0);
+            if (leader) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma(tmem_base + j * C::T_COLS,
+                       dq + ((j * C::NB + (kk >> 2)) * C::QBOX >> 4) + 2 * (kk & 3),
+                       bk + ((kk >> 2) * C::KBOX >> 4) + 2 * (kk & 3), id_s, kk > 0 ? 1u : 0u);
+              tc_commit(tbar(j, 0));
+            }
+            __syncwarp();
+            ++cs[j];
           }
           if (!ok) break;
-          tc_commit(bar(C::B_E + i % C::ST));
+          if (leader) {
+            tc_commit(rbar(ks, 0, 1));
+            if (t + 2 == nt) tc_commit(bar(C::B_QE));
+          }
+          __syncwarp();
+          if (++ks == C::NP) {
+            ks = 0;
+            kph ^= 1u;
+          }
         }
-        n += 2 * nt;
+        if (t < 0) continue;
+        ok = kc_wait(rbar(vs, 1, 0), vph, abort_flag, lim);
+        if (!ok) break;
+        const uint64_t bv = dv + (uint64_t)(uint32_t)(vs * (2 * C::SLOT >> 4));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (j >= nj) break;
+          ok = kc_wait(tbar(j, 2), cv[j] & 1u, abort_flag, lim);
+          if (!ok) break;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              tc_mma_ts(tmem_base + C::O_COL + j * D, tmem_base + j * C::T_COLS + BN + kk * 8,
+                        bv + kk * (2048 >> 4), id_o, (t > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(tbar(j, 3));
+          }
+          __syncwarp();
+          ++cv[j];
+        }
+        if (!ok) break;
+        if (leader) tc_commit(rbar(vs, 1, 1));
+        __syncwarp();
+        if (++vs == C::NP) {
+          vs = 0;
+          vph ^= 1u;
+        }
       }
-      if (!ok) {
-        atomicExch(a.err, DEV_TIMEOUT_MMA);
-        *abort_flag = 1;
-      }
+    }
+    if (!ok && lane == 0) {
+      atomicExch(a.err, DEV_TIMEOUT_MMA);
+      *abort_flag = 1;
+    }
+    if (leader) {
       tc_commit(bar(C::B_DRAIN));
       volatile int never = 0;
       mbar_wait(bar(C::B_DRAIN), 0, &never, lim);
     }
+    __syncwarp();
   } else {
     // ---------------------------------------------------------- softmax
-    const int j = (warp - 2) >> 2;            // row tile of this warpgroup
+    const int j = (warp - 4) >> 2;            // row tile of this warpgroup
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;        // packed row (TMEM lane)
     const int rq = r / a.G, rg = r - rq * a.G;
@@ -390,6 +484,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         for (int e = 0; e < BN / 2; ++e) pk[e] = kc_pack(s[2 * e], s[2 * e + 1]);
 #pragma unroll
         for (int c = 0; c + 32 <= BN / 2; c += 32) tmem_st32_u(t_p + c, pk + c);
+        if constexpr (BN / 2 % 32 == 16) tmem_st16_u(t_p + BN / 2 - 16, pk + BN / 2 - 16);
         if constexpr (BN / 2 % 32 == 8) tmem_st8_u(t_p + BN / 2 - 8, pk + BN / 2 - 8);
         tmem_wait_st();
         tc_fence_before();
@@ -459,7 +554,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
 namespace {
 template <int D> struct KcBn;                 // key tile: S, P and O of two row tiles fill TMEM
 template <> struct KcBn<128> { static constexpr int v = 80; };
-template <> struct KcBn<64> { static constexpr int v = 128; };
+template <> struct KcBn<64> { static constexpr int v = 96; };
 
 template <int D> cudaError_t run_tc(const KeyArgs &a, cudaStream_t s) {
   constexpr int BN = KcBn<D>::v;
@@ -471,9 +566,7 @@ template <int D> cudaError_t run_tc(const KeyArgs &a, cudaStream_t s) {
   const long long rows = (long long)a.batch * a.n_ctx;
   bool ok = tma_encode_heads(&p.q, a.q, a.M, a.H, D, a.ld_q, a.G, QR) &&
             tma_encode_rows(&p.k, a.k, rows, a.Hkv * D, a.ld_kv, BN) &&
-            tma_encode_rows(&p.v, a.v, rows, a.Hkv * D, a.ld_kv, BN) &&
-            tma_encode_rows(&p.kg, a.k, rows, a.Hkv * D, a.ld_kv, 1) &&
-            tma_encode_rows(&p.vg, a.v, rows, a.Hkv * D, a.ld_kv, 1);
+            tma_encode_rows(&p.v, a.v, rows, a.Hkv * D, a.ld_kv, BN);
   if (ok && a.prefix_len > 0)
     ok = tma_encode_rows(&p.kp, a.kp, a.prefix_len, a.Hkv * D, a.ld_p, BN) &&
          tma_encode_rows(&p.vp, a.vp, a.prefix_len, a.Hkv * D, a.ld_p, BN);
