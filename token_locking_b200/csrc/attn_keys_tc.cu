@@ -4,16 +4,18 @@
 // A unit is two tiles of 128 packed rows (query row, head of the group) of one
 // K/V head against a list of tiles of BN keys; a CTA takes an equal share of
 // all units' tiles (keys_plan.cuh) and runs through its pieces without a break:
-//   warps 0,2,3  producers.  Warp 0 copies Q by TMA in boxes [QR query rows]
+//   warps 0,3    producers.  Warp 0 copies Q by TMA in boxes [QR query rows]
 //                [G heads][64], so that packed rows land in order whatever G,
 //                and every full tile of the prefix or of an unlisted cache.
 //                Listed keys, and the tile a key set ends in, are copied row by
-//                row by all three warps (16-byte asynchronous copies, three tiles
+//                row by both warps (16-byte asynchronous copies, three tiles
 //                in flight), zeros for entries that are not there: what lies
 //                behind a key set never reaches shared memory.  (Four-row TMA
 //                gathers instead took 17 clocks a row of 128 bytes, 7200 clocks
 //                a tile.)
-//   warp 1       owns TMEM; one lane issues S_j = Q_j K^T and O_j += P_j V
+//   warps 1,2    one lane each issues S_j = Q_j K^T and O_j += P_j V of row tile
+//                j (warp 1 owns TMEM).  One issuing warp for both tiles took
+//                some 2500 clocks a tile of keys, in waits and issue alone.
 //   warps 4..11  a softmax warpgroup per row tile j, one row per thread: the
 //                running maximum and sum need no shuffles.  The maximum is
 //                raised only when a tile exceeds it by 2^8 (O is rescaled then);
@@ -48,13 +50,12 @@ template <int D, int BN> struct KcCfg {
   static constexpr int NP = (232448 - 1024 - TAIL - KV_OFF) / (2 * SLOT);
   static constexpr int BAR_OFF = KV_OFF + 2 * NP * SLOT;
   static constexpr int SMEM = BAR_OFF + TAIL + 1024;    // + alignment
-  // barriers: Q full, Q free; per stage K full, K free, V full, V free
-  static constexpr int B_QF = 0, B_QE = 1, B_RING = 2, B_TILE = 2 + 4 * NP;
-  static constexpr int B_DRAIN = B_TILE + 8, B_COUNT = B_DRAIN + 1;
-  // row copies: 16-byte chunks of a row, rows of a warp instruction, tiles a
-  // warp keeps in flight
-  static constexpr int CH = D / 8, RPI = 32 / CH, LAG = 3;
-  static constexpr int NI = (BN / RPI + 2) / 3;         // instructions of a warp, at most
+  // barriers: Q full, Q free; per stage full, free; per row tile four; drain
+  static constexpr int B_QF = 0, B_QE = 1, B_F = 2, B_E = 2 + NP, B_TILE = 2 + 2 * NP;
+  static constexpr int B_DRAIN = B_TILE + 8, B_COUNT = B_DRAIN + 2;
+  // row copies: 16-byte chunks of a row, rows of a warp instruction, instructions
+  // of each of the two warps, tiles in flight
+  static constexpr int CH = D / 8, RPI = 32 / CH, NI = BN / RPI / 2, LAG = 3;
   static constexpr int PLAN_OFF = BAR_OFF + 512;
   // TMEM columns: per row tile S, then P (two bf16 keys a column), from a
   // multiple of 64; then O of both
@@ -62,7 +63,7 @@ template <int D, int BN> struct KcCfg {
   static constexpr uint32_t O_COL = 2 * T_COLS;
   static_assert(O_COL + 2 * D <= 512, "TMEM columns");
   static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
-  static_assert(NI * RPI <= 32, "a lane per row of a warp's share");
+  static_assert(BN % (2 * RPI) == 0 && NI * RPI <= 64, "two rows a lane of a warp's share");
   static_assert(LAG < NP, "row copies in flight");
   static_assert(SMEM <= 232448 && BN % 16 == 0, "shared memory, key tile");
 };
@@ -86,9 +87,16 @@ __device__ __forceinline__ uint32_t kc_pack(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// All lanes wait; the outcome is the same for all.  The waiting loop is kept out
+// of line: the roles' code competes for the instruction caches.
+__device__ __noinline__ bool kc_wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                          unsigned long long lim) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, lim));
+}
 __device__ __forceinline__ bool kc_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
                                         unsigned long long lim) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, lim));
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  return kc_wait_long(bar, parity, abort_flag, lim);
 }
 
 // One lane of the warp (the same every time).
@@ -122,10 +130,6 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
   // per row tile: 0 scores ready, 1 scores read, 2 P written, 3 P V done
   auto tbar = [&](int j, int k) { return bar0 + 8u * (uint32_t)(C::B_TILE + 4 * j + k); };
-  // stage s: K (0) or V (1), full (0) or free (1)
-  auto rbar = [&](int s, int kv, int e) {
-    return bar0 + 8u * (uint32_t)(C::B_RING + 4 * s + 2 * kv + e);
-  };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::B_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   KeyPlan &pl = *reinterpret_cast<KeyPlan *>(smem + C::PLAN_OFF);
@@ -136,12 +140,11 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
 
   if (threadIdx.x == 0) {
     mbar_init(bar(C::B_QF), 1);
-    mbar_init(bar(C::B_QE), 1);
-    for (int s = 0; s < C::NP; ++s)
-      for (int kv = 0; kv < 2; ++kv) {
-        mbar_init(rbar(s, kv, 0), 3);         // the three producer warps
-        mbar_init(rbar(s, kv, 1), 1);         // MMA commit
-      }
+    mbar_init(bar(C::B_QE), 2);               // both issuing warps
+    for (int s = 0; s < C::NP; ++s) {
+      mbar_init(bar(C::B_F + s), 2);          // both producers
+      mbar_init(bar(C::B_E + s), 2);
+    }
     for (int j = 0; j < 2; ++j) {
       mbar_init(tbar(j, 0), 1);               // MMA commit
       mbar_init(tbar(j, 1), 4);               // the tile's four softmax warps
@@ -149,6 +152,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       mbar_init(tbar(j, 3), 1);
     }
     mbar_init(bar(C::B_DRAIN), 1);
+    mbar_init(bar(C::B_DRAIN + 1), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&p.q);
@@ -184,27 +188,30 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     return rn > QR ? 2 : 1;
   };
 
-  if (warp == 0 || warp == 2 || warp == 3) {
+  if (warp == 0 || warp == 3) {
     // --------------------------------------------------------- producers
-    const int pw = warp == 0 ? 0 : warp - 1;  // 0..2
+    const int pw = warp == 0 ? 0 : 1;
     const int g0 = lane / C::CH, ch = lane % C::CH;
-    // instruction i of this warp copies rows (3 i + pw) RPI + g0; lane l holds
-    // the cache position of the l-th row of the warp's share
-    const int my_row = (3 * (lane / C::RPI) + pw) * C::RPI + lane % C::RPI;
-    int st = 0, np = 0, n = 0;                // stage, pieces, tiles
+    // instruction i of this warp copies rows (2 i + pw) RPI + g0; lane l holds
+    // the cache positions of the l-th and (32 + l)-th row of the warp's share
+    const int my_row = (2 * (lane / C::RPI) + pw) * C::RPI + lane % C::RPI;
+    const int my_row2 = my_row + 64;          // 32 rows of the share later
+    // where this lane's chunk goes: rows advance by 2 RPI, a multiple of 4
+    const uint32_t off = (ch >> 3) * C::KBOX + (pw * C::RPI + g0) * 128;
+    const uint32_t sw0 = ((ch ^ (pw * C::RPI + g0)) & 7) << 4, sw1 = sw0 ^ (4 << 4);
+    int st = 0, np = 0;                       // stage, pieces
     uint32_t ph = 0;
     bool ok = true;
     while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
       int r0, rn;
       const int nj = rows_of(r0, rn), b = kp_seq(pl, pc.job);
-      // position of this lane's row in tile t's copy, -1 where there is none
-      auto entry = [&](int t) {
+      // position of row r of tile t, -1 where there is none
+      auto entry = [&](int t, int r) {
         const bool pre = b < 0 || (!pl.stacked && t < tp);
-        const int i = (pl.stacked ? t : t - tp) * BN + my_row;
-        if (pre || t >= pc.t1 || lane >= C::NI * C::RPI || my_row >= BN || i >= pl.kl[b]) return -1;
-        return key_pos(a, b, i);
+        const int i = (pl.stacked ? t : t - tp) * BN + r;
+        return pre || t >= pc.t1 || r >= BN || i >= pl.kl[b] ? -1 : key_pos(a, b, i);
       };
-      int nxt = entry(pc.t0);
+      int nxt = entry(pc.t0, my_row), nxt2 = entry(pc.t0, my_row2);
       if (pw == 0) {
         if (!kc_wait(bar(C::B_QE), (uint32_t)(np & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
         if (lane == 0) {
@@ -222,71 +229,58 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       auto hand_over = [&]() {
         fence_proxy_async_smem();             // written by copies, read by the tensor cores
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(rbar(pst, 0, 0));
-          mbar_arrive(rbar(pst, 1, 0));
-        }
+        if (lane == 0) mbar_arrive(bar(C::B_F + pst));
         pst = pst + 1 == C::NP ? 0 : pst + 1;
         --pend;
       };
-      for (int t = pc.t0; t < pc.t1; ++t, ++n) {
+      for (int t = pc.t0; t < pc.t1; ++t) {
         const bool pre = b < 0 || (!pl.stacked && t < tp);
         const int i0 = (pre || pl.stacked ? t : t - tp) * BN;
         const bool by_row = !pre && (a.keys || i0 + BN > pl.kl[b]);
-        const int pos = nxt;
-        nxt = entry(t + 1);
+        const int pos = nxt, pos2 = nxt2;
+        nxt = entry(t + 1, my_row);
+        nxt2 = entry(t + 1, my_row2);
         const uint32_t dst = sbase + C::KV_OFF + 2 * st * C::SLOT;
+        if (!by_row && pend > 0) {
+          kc_copy_wait<0>();
+          while (pend > 0) hand_over();
+        }
+        if (!kc_wait(bar(C::B_E + st), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
         if (by_row) {
+          const long long base = (long long)b * a.n_ctx * a.ld_kv + pc.hk * D + ch * 8;
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            if (!kc_wait(rbar(st, kv, 1), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
-            const bf16 *src = (const bf16 *)(kv ? a.v : a.k) + (long long)b * a.n_ctx * a.ld_kv +
-                              pc.hk * D + ch * 8;
-            const uint32_t d0 = dst + kv * C::SLOT + (ch >> 3) * C::KBOX;
+            const bf16 *src = (const bf16 *)(kv ? a.v : a.k) + base;
+            const uint32_t d0 = dst + kv * C::SLOT + off;
 #pragma unroll
             for (int i = 0; i < C::NI; ++i) {
-              const int ps = __shfl_sync(0xffffffffu, pos, i * C::RPI + g0);
-              const int row = (3 * i + pw) * C::RPI + g0;
-              if (row < BN)
-                kc_copy16(d0 + row * 128 + (((ch ^ row) & 7) << 4),
-                          src + (ps < 0 ? 0 : ps) * a.ld_kv, ps >= 0);
+              const int ps = i * C::RPI < 32
+                                 ? __shfl_sync(0xffffffffu, pos, (i * C::RPI + g0) & 31)
+                                 : __shfl_sync(0xffffffffu, pos2, (i * C::RPI + g0) & 31);
+              kc_copy16(d0 + i * 2 * C::RPI * 128 + ((i * 2 * C::RPI) & 4 ? sw1 : sw0),
+                        src + (ps < 0 ? 0 : ps) * a.ld_kv, ps >= 0);
             }
           }
-          if (!ok) break;
           kc_copy_commit();
           if (++pend == C::LAG) {
             kc_copy_wait<C::LAG - 1>();
             hand_over();
           }
         } else {
-          if (pend > 0) {
-            kc_copy_wait<0>();
-            while (pend > 0) hand_over();
-          }
-          if (pw == 0) {
-            const int y = pre ? i0 : b * a.n_ctx + i0;
+          if (lane == 0) {
+            if (pw == 0) {
+              const int y = pre ? i0 : b * a.n_ctx + i0;
+              mbar_expect_tx(bar(C::B_F + st), 2 * C::SLOT);
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              if (!kc_wait(rbar(st, kv, 1), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
-              if (lane == 0) {
+              for (int kv = 0; kv < 2; ++kv) {
                 const CUtensorMap *m = pre ? (kv ? &p.vp : &p.kp) : (kv ? &p.v : &p.k);
-                mbar_expect_tx(rbar(st, kv, 0), C::SLOT);
 #pragma unroll
                 for (int c = 0; c < C::NB; ++c)
                   tma_load_2d(dst + kv * C::SLOT + c * C::KBOX, m, pc.hk * D + 64 * c, y,
-                              rbar(st, kv, 0));
+                              bar(C::B_F + st));
               }
-            }
-            if (!ok) break;
-          } else {
-            if (!kc_wait(rbar(st, 0, 1), ph ^ 1u, abort_flag, lim) ||
-                !kc_wait(rbar(st, 1, 1), ph ^ 1u, abort_flag, lim)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              mbar_arrive(rbar(st, 0, 0));
-              mbar_arrive(rbar(st, 1, 0));
+            } else {
+              mbar_arrive(bar(C::B_F + st));
             }
           }
           pst = st + 1 == C::NP ? 0 : st + 1;
@@ -307,64 +301,57 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       atomicExch(a.err, DEV_TIMEOUT_PRODUCER);
       *abort_flag = 1;
     }
-    // Every copy lands before the CTA can exit: the MMA warp has waited for each
-    // stage, unless a wait ran out.  Then the stages' last fills are waited for
-    // here; one that not every producer handed over costs its share of the limit.
+    // Every copy lands before the CTA can exit: the issuing warps have waited for
+    // each stage, unless a wait ran out.  Then the stages' last fills are waited
+    // for here; one that not both producers handed over costs its share of the limit.
     if (pw == 0 && lane == 0 && *abort_flag) {
       volatile int never = 0;
       if (np > 0) mbar_wait(bar(C::B_QF), (uint32_t)(np - 1) & 1u, &never, lim);
       for (int s = 0; s < C::NP; ++s)
-        for (int kv = 0; kv < 2; ++kv)
-          mbar_wait(rbar(s, kv, 0), s <= st ? ph : ph ^ 1u, &never, lim / (2 * C::NP));
+        mbar_wait(bar(C::B_F + s), s <= st ? ph : ph ^ 1u, &never, lim / C::NP);
     }
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // ------------------------------------------------------------- MMA
+    const int j = warp - 1;                   // row tile
     constexpr uint32_t id_s = idesc_bf16_f32<BN>();
     constexpr uint32_t id_o = idesc_bf16_f32_bmn<D>();
     const bool leader = kc_elect();
-    const uint64_t dq = smem_desc_sw128(sbase);
+    const uint64_t dq = smem_desc_sw128(sbase + j * C::NB * C::QBOX);
     const uint64_t dk = smem_desc_sw128(sbase + C::KV_OFF);
     const uint64_t dv = smem_desc_sw128_mn(sbase + C::KV_OFF + C::SLOT, C::KBOX, 1024);
+    const uint32_t t_s = tmem_base + j * C::T_COLS, t_o = tmem_base + C::O_COL + j * D;
     int np = 0;
     int ks = 0, vs = 0;                       // stages of the next scores and P V product
-    uint32_t kph = 0, vph = 0;
-    uint32_t cs[2] = {0u, 0u}, cv[2] = {0u, 0u};   // scores and P V products issued
+    uint32_t kph = 0;
+    uint32_t cs = 0, cv = 0;                  // scores and P V products issued, parities
     bool ok = true;
     while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
       int r0, rn;
-      const int nj = rows_of(r0, rn);
+      const bool mine = j < rows_of(r0, rn);
       const int nt = pc.t1 - pc.t0;
       ok = kc_wait(bar(C::B_QF), (uint32_t)(np & 1), abort_flag, lim);
       ++np;
       // scores of tile t are issued one tile ahead of its P V product
       for (int t = -1; ok && t < nt; ++t) {
         if (t + 1 < nt) {
-          ok = kc_wait(rbar(ks, 0, 0), kph, abort_flag, lim);
+          ok = kc_wait(bar(C::B_F + ks), kph, abort_flag, lim);
           if (!ok) break;
-          const uint64_t bk = dk + (uint64_t)(uint32_t)(ks * (2 * C::SLOT >> 4));
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (j >= nj) break;
+          if (mine) {
             // the buffer's last scores have been read
-            ok = kc_wait(tbar(j, 1), (cs[j] & 1u) ^ 1u, abort_flag, lim);
+            ok = kc_wait(tbar(j, 1), cs ^ 1u, abort_flag, lim);
             if (!ok) break;
             tc_fence_after();
+            const uint64_t bk = dk + (uint64_t)(uint32_t)(ks * (2 * C::SLOT >> 4));
             if (leader) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk)
-                tc_mma(tmem_base + j * C::T_COLS,
-                       dq + ((j * C::NB + (kk >> 2)) * C::QBOX >> 4) + 2 * (kk & 3),
+                tc_mma(t_s, dq + ((kk >> 2) * C::QBOX >> 4) + 2 * (kk & 3),
                        bk + ((kk >> 2) * C::KBOX >> 4) + 2 * (kk & 3), id_s, kk > 0 ? 1u : 0u);
               tc_commit(tbar(j, 0));
             }
-            __syncwarp();
-            ++cs[j];
+            cs ^= 1u;
           }
-          if (!ok) break;
-          if (leader) {
-            tc_commit(rbar(ks, 0, 1));
-            if (t + 2 == nt) tc_commit(bar(C::B_QE));
-          }
+          if (t + 2 == nt && leader) tc_commit(bar(C::B_QE));
           __syncwarp();
           if (++ks == C::NP) {
             ks = 0;
@@ -372,32 +359,23 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
           }
         }
         if (t < 0) continue;
-        ok = kc_wait(rbar(vs, 1, 0), vph, abort_flag, lim);
-        if (!ok) break;
-        const uint64_t bv = dv + (uint64_t)(uint32_t)(vs * (2 * C::SLOT >> 4));
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (j >= nj) break;
-          ok = kc_wait(tbar(j, 2), cv[j] & 1u, abort_flag, lim);
+        if (mine) {
+          ok = kc_wait(tbar(j, 2), cv, abort_flag, lim);
           if (!ok) break;
           tc_fence_after();
+          const uint64_t bv = dv + (uint64_t)(uint32_t)(vs * (2 * C::SLOT >> 4));
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-              tc_mma_ts(tmem_base + C::O_COL + j * D, tmem_base + j * C::T_COLS + BN + kk * 8,
-                        bv + kk * (2048 >> 4), id_o, (t > 0 || kk > 0) ? 1u : 0u);
+              tc_mma_ts(t_o, t_s + BN + kk * 8, bv + kk * (2048 >> 4), id_o,
+                        (t > 0 || kk > 0) ? 1u : 0u);
             tc_commit(tbar(j, 3));
           }
-          __syncwarp();
-          ++cv[j];
+          cv ^= 1u;
         }
-        if (!ok) break;
-        if (leader) tc_commit(rbar(vs, 1, 1));
+        if (leader) tc_commit(bar(C::B_E + vs));   // done with the stage
         __syncwarp();
-        if (++vs == C::NP) {
-          vs = 0;
-          vph ^= 1u;
-        }
+        if (++vs == C::NP) vs = 0;
       }
     }
     if (!ok && lane == 0) {
@@ -405,9 +383,9 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       *abort_flag = 1;
     }
     if (leader) {
-      tc_commit(bar(C::B_DRAIN));
+      tc_commit(bar(C::B_DRAIN + j));
       volatile int never = 0;
-      mbar_wait(bar(C::B_DRAIN), 0, &never, lim);
+      mbar_wait(bar(C::B_DRAIN + j), 0, &never, lim);
     }
     __syncwarp();
   } else {
