@@ -16,11 +16,14 @@
 //   warps 1,2    one lane each issues S_j = Q_j K^T and O_j += P_j V of row tile
 //                j (warp 1 owns TMEM).  One issuing warp for both tiles took
 //                some 2500 clocks a tile of keys, in waits and issue alone.
-//   warps 4..11  a softmax warpgroup per row tile j, one row per thread: the
-//                running maximum and sum need no shuffles.  The maximum is
-//                raised only when a tile exceeds it by 2^8 (O is rescaled then);
-//                p is rounded to bf16 for the product (half a step, 2^-9
-//                relative on average), its sum is taken in fp32 before that.
+//   warps 4..19  softmax: two warpgroups per row tile, a row per thread in
+//                each and half of the tile's keys; both take the maximum over
+//                all of them, so they need not meet but at the end, for the row's
+//                sum.  (One warpgroup per tile, all keys: 2300 clocks per 80 keys,
+//                with two warps per scheduler too few to keep the exponentials
+//                running through the waits.)  The maximum is raised only when a
+//                tile exceeds it by 2^8 (O is rescaled then); p is rounded to
+//                bf16 for the product (half a step), its sum taken in fp32 before.
 // The two row tiles are two independent chains (scores, softmax, P V) that
 // share K and V, so that the tensor cores work on one while the other's
 // exponentials are taken.
@@ -37,7 +40,7 @@ namespace sl {
 
 namespace {
 constexpr int KC_ROWS = 128;                  // packed rows of a tile (TMEM lanes)
-constexpr int KC_THREADS = 128 + 2 * 128;
+constexpr int KC_THREADS = 128 + 4 * 128;
 constexpr float KC_RESCALE = 8.f;
 
 template <int D, int BN> struct KcCfg {
@@ -61,7 +64,9 @@ template <int D, int BN> struct KcCfg {
   // multiple of 64; then O of both
   static constexpr uint32_t T_COLS = (BN + BN / 2 + 63) / 64 * 64;
   static constexpr uint32_t O_COL = 2 * T_COLS;
-  static_assert(O_COL + 2 * D <= 512, "TMEM columns");
+  static constexpr uint32_t L_COL = BN + BN / 2;        // the two halves' row sums
+  static_assert(O_COL + 2 * D <= 512 && L_COL + 2 <= T_COLS, "TMEM columns");
+  static constexpr int HB = BN / 2;                     // keys of a softmax warpgroup
   static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
   static_assert(BN % (2 * RPI) == 0 && NI * RPI <= 64, "two rows a lane of a warp's share");
   static_assert(LAG < NP, "row copies in flight");
@@ -74,12 +79,31 @@ struct KcParams {
   KeyArgs a;
 };
 
-// N fp32 columns of this thread's TMEM lane (N a multiple of 16), one wait.
+// N fp32 columns of this thread's TMEM lane (N a multiple of 8), one wait.
 template <int N> __device__ __forceinline__ void tmem_ld_cols(uint32_t t, float *s) {
 #pragma unroll
   for (int c = 0; c + 32 <= N; c += 32) tmem_ld32_nw(t + c, s + c);
-  if constexpr (N % 32 == 16) tmem_ld16_nw(t + N - 16, s + N - 16);
+  if constexpr (N % 32 >= 16) tmem_ld16_nw(t + N / 32 * 32, s + N / 32 * 32);
+  if constexpr (N % 16 == 8) tmem_ld8_nw(t + N - 8, s + N - 8);
   tmem_wait_ld();
+}
+// N columns of it (N a multiple of 4), without a wait.
+template <int N> __device__ __forceinline__ void tmem_st_cols(uint32_t t, const uint32_t *r) {
+  static_assert(N < 32 && N % 4 == 0, "columns");
+  if constexpr (N >= 16) tmem_st16_u(t, r);
+  if constexpr (N % 16 >= 8) tmem_st8_u(t + N / 16 * 16, r + N / 16 * 16);
+  if constexpr (N % 8 == 4) tmem_st4_u(t + N - 4, r + N - 4);
+}
+// The largest of s[0..N) (N even).
+template <int N> __device__ __forceinline__ float max_of(const float *s) {
+  float a = s[0], b = s[1];
+#pragma unroll
+  for (int i = 2; i + 3 < N; i += 4) {
+    a = max3(a, s[i], s[i + 1]);
+    b = max3(b, s[i + 2], s[i + 3]);
+  }
+  if constexpr (N % 4 == 0) a = max3(a, s[N - 2], s[N - 1]);
+  return fmaxf(a, b);
 }
 
 __device__ __forceinline__ uint32_t kc_pack(float lo, float hi) {
@@ -147,8 +171,8 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     }
     for (int j = 0; j < 2; ++j) {
       mbar_init(tbar(j, 0), 1);               // MMA commit
-      mbar_init(tbar(j, 1), 4);               // the tile's four softmax warps
-      mbar_init(tbar(j, 2), 4);
+      mbar_init(tbar(j, 1), 8);               // the tile's eight softmax warps
+      mbar_init(tbar(j, 2), 8);
       mbar_init(tbar(j, 3), 1);
     }
     mbar_init(bar(C::B_DRAIN), 1);
@@ -390,63 +414,82 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     __syncwarp();
   } else {
     // ---------------------------------------------------------- softmax
-    const int j = (warp - 4) >> 2;            // row tile of this warpgroup
+    constexpr int HB = C::HB;
+    const int j = (warp - 4) >> 3;            // row tile
+    const int half = (warp - 4) >> 2 & 1;     // keys half HB .. half HB + HB of a tile
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;        // packed row (TMEM lane)
     const int rq = r / a.G, rg = r - rq * a.G;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t t_s = tmem_base + lane_off + j * C::T_COLS;
-    const uint32_t t_o = tmem_base + lane_off + C::O_COL + j * D;
-    const uint32_t t_p = t_s + BN;
+    const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + j * C::T_COLS;
+    const uint32_t t_s = t_row + half * HB;
+    const uint32_t t_p = t_row + BN + half * (HB / 2);
+    const uint32_t t_o = tmem_base + ((uint32_t)(quarter * 32) << 16) + C::O_COL + j * D +
+                         half * (D / 2);      // this warpgroup's columns of O
     const float c2 = a.scale * KEY_LOG2E;
     const size_t slot_f = (size_t)2 * QR * a.G * (D + 2);
     uint32_t cs = 0;                          // score tiles taken
+    // After a wait that ran out the loops go on without waiting (the abort flag
+    // ends later waits at once), so that both halves of a tile meet below.
     bool ok = true;
-    while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+    auto wait = [&](int k, uint32_t parity) {
+      if (!ok) return;
+      ok = kc_wait(tbar(j, k), parity, abort_flag, lim);
+      if (!ok && lane == 0) {
+        atomicExch(a.err, DEV_TIMEOUT_EPI);
+        *abort_flag = 1;
+      }
+    };
+    while (key_next(pl, a.Hkv, w, w_end, job, pc)) {
       int r0, rn;
       if (rows_of(r0, rn) <= j) continue;
       const int b = kp_seq(pl, pc.job);
       float m = -INFINITY, l = 0.f;
-      float s[BN];
       for (int t = pc.t0; t < pc.t1; ++t, ++cs) {
         const bool pre = b < 0 || (!pl.stacked && t < tp);
         const int nv = (pre ? a.prefix_len : pl.kl[b]) - (pre || pl.stacked ? t : t - tp) * BN;
-        if (!kc_wait(tbar(j, 0), cs & 1u, abort_flag, lim)) { ok = false; break; }
+        wait(0, cs & 1u);
         tc_fence_after();
-        tmem_ld_cols<BN>(t_s, s);
+        float s[HB];
+        // the other half's keys for the maximum, then this one's
+        tmem_ld_cols<HB>(t_row + (half ^ 1) * HB, s);
+        if (nv < BN) {
+#pragma unroll
+          for (int i = 0; i < HB; ++i) s[i] = (half ^ 1) * HB + i < nv ? s[i] : -INFINITY;
+        }
+        float mt = max_of<HB>(s);
+        tmem_ld_cols<HB>(t_s, s);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(tbar(j, 1));
         if (nv < BN) {
 #pragma unroll
-          for (int i = 0; i < BN; ++i) s[i] = i < nv ? s[i] : -INFINITY;
+          for (int i = 0; i < HB; ++i) s[i] = half * HB + i < nv ? s[i] : -INFINITY;
         }
-        float mx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx[e] = s[e];
-#pragma unroll
-        for (int i = 8; i < BN; ++i) mx[i & 7] = fmaxf(mx[i & 7], s[i]);
-        const float mt = c2 * fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                    fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        mt = c2 * fmaxf(mt, max_of<HB>(s));
         const bool first = t == pc.t0;
         const float m_new = fmaxf(m, mt);
         const bool resc = !first && m_new > m + KC_RESCALE;
         const float m_use = (first || resc) ? m_new : m;
         const float alpha = resc ? (m == -INFINITY ? 0.f : ex2_approx(m - m_new)) : 1.f;
-        const float m_sub = m_use == -INFINITY ? 0.f : m_use;   // all scores -inf: p = 0
-        float sm[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const float m_sub = m_use == -INFINITY ? 0.f : -m_use;  // all scores -inf: p = 0
+        float sa[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[HB / 2];
 #pragma unroll
-        for (int i = 0; i < BN; ++i) {
-          s[i] = ex2_approx(fmaf(s[i], c2, -m_sub));
-          sm[i & 7] += s[i];
+        for (int i = 0; i < HB; i += 2) {
+          fma2(s[i], s[i + 1], c2, m_sub);
+          s[i] = ex2_approx(s[i]);
+          s[i + 1] = ex2_approx(s[i + 1]);
+          add2(sa[i & 2], sa[(i & 2) + 1], s[i], s[i + 1]);
+          pk[i / 2] = kc_pack(s[i], s[i + 1]);
         }
-        const float rs = ((sm[0] + sm[1]) + (sm[2] + sm[3])) + ((sm[4] + sm[5]) + (sm[6] + sm[7]));
+        l = l * alpha + ((sa[0] + sa[1]) + (sa[2] + sa[3]));
+        m = m_use;
         // the last P V product has read P and written O
-        if (!first && !kc_wait(tbar(j, 3), (cs & 1u) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        if (!first) wait(3, (cs & 1u) ^ 1u);
         tc_fence_after();
         if (__any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+          for (int c = 0; c < D / 2; c += 32) {
             float o[32];
             tmem_ld32_nw(t_o + c, o);
             tmem_wait_ld();
@@ -455,44 +498,44 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
             tmem_st32(t_o + c, o);
           }
         }
-        l = l * alpha + rs;
-        m = m_use;
-        uint32_t pk[BN / 2];
-#pragma unroll
-        for (int e = 0; e < BN / 2; ++e) pk[e] = kc_pack(s[2 * e], s[2 * e + 1]);
-#pragma unroll
-        for (int c = 0; c + 32 <= BN / 2; c += 32) tmem_st32_u(t_p + c, pk + c);
-        if constexpr (BN / 2 % 32 == 16) tmem_st16_u(t_p + BN / 2 - 16, pk + BN / 2 - 16);
-        if constexpr (BN / 2 % 32 == 8) tmem_st8_u(t_p + BN / 2 - 8, pk + BN / 2 - 8);
+        tmem_st_cols<HB / 2>(t_p, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(tbar(j, 2));
       }
-      if (!ok) break;
-      if (!kc_wait(tbar(j, 3), (cs - 1u) & 1u, abort_flag, lim)) { ok = false; break; }
+      // the row's sum: both halves' through TMEM
+      wait(3, (cs - 1u) & 1u);
       tc_fence_after();
-      // O leaves in 64-column parts: final rows of a whole unit, else partial ones
+      tmem_st1_u(t_row + C::L_COL + half, __float_as_uint(l));
+      tmem_wait_st();
+      tc_fence_before();
+      named_bar_sync(1 + j * 4 + quarter, 64);
+      tc_fence_after();
+      l += __uint_as_float(tmem_ld1_u(t_row + C::L_COL + (half ^ 1)));
+      if (!ok) continue;
+      // O leaves in 32-column parts: final rows of a whole unit, else partial ones
       const bool live = rq < QR && j * QR + rq < rn;
       const int row = r0 + j * QR + rq, h = pc.hk * a.G + rg;
       const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
+      float o[32];
       if (whole && !pl.stacked) {
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        bf16 *orow = (bf16 *)a.o + row * a.ld_o + h * D;
+        bf16 *orow = (bf16 *)a.o + row * a.ld_o + h * D + half * (D / 2);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          tmem_ld_cols<64>(t_o + c0, s);
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+          tmem_ld_cols<32>(t_o + c0, o);
           if (live) {
             uint4 *dst = reinterpret_cast<uint4 *>(orow + c0);
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-              dst[c] = make_uint4(kc_pack(s[8 * c] * inv, s[8 * c + 1] * inv),
-                                  kc_pack(s[8 * c + 2] * inv, s[8 * c + 3] * inv),
-                                  kc_pack(s[8 * c + 4] * inv, s[8 * c + 5] * inv),
-                                  kc_pack(s[8 * c + 6] * inv, s[8 * c + 7] * inv));
+            for (int c = 0; c < 4; ++c)
+              dst[c] = make_uint4(kc_pack(o[8 * c] * inv, o[8 * c + 1] * inv),
+                                  kc_pack(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
+                                  kc_pack(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
+                                  kc_pack(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
           }
         }
-        if (live && a.lse)
+        if (live && a.lse && half == 0)
           a.lse[(size_t)row * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * KEY_LN2;
       } else {
         float *rec = whole ? a.ws + 2 * (size_t)gridDim.x * slot_f +
@@ -500,20 +543,16 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
                            : a.ws + kp_slot(blockIdx.x, pc.t0) * slot_f +
                                  (size_t)(j * QR * a.G + r) * (D + 2);
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          tmem_ld_cols<64>(t_o + c0, s);
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+          tmem_ld_cols<32>(t_o + c0, o);
           if (live) {
-            float2 *dst = reinterpret_cast<float2 *>(rec + 2 + c0);
+            float2 *dst = reinterpret_cast<float2 *>(rec + 2 + half * (D / 2) + c0);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) dst[c] = make_float2(s[2 * c], s[2 * c + 1]);
+            for (int c = 0; c < 16; ++c) dst[c] = make_float2(o[2 * c], o[2 * c + 1]);
           }
         }
-        if (live) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);
+        if (live && half == 0) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);
       }
-    }
-    if (!ok && lane == 0) {
-      atomicExch(a.err, DEV_TIMEOUT_EPI);
-      *abort_flag = 1;
     }
   }
 

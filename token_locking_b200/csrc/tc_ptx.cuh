@@ -214,6 +214,15 @@ __device__ __forceinline__ void tmem_ld16_nw(uint32_t taddr, float *v) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// 8 columns of it.
+__device__ __forceinline__ void tmem_ld8_nw(uint32_t taddr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -242,7 +251,7 @@ __device__ __forceinline__ void tmem_st32_u(uint32_t taddr, const uint32_t *r) {
       "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
-// 16 and 8 columns of it.
+// 16, 8 and 4 columns of it.
 __device__ __forceinline__ void tmem_st16_u(uint32_t taddr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
@@ -258,8 +267,44 @@ __device__ __forceinline__ void tmem_st8_u(uint32_t taddr, const uint32_t *r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st4_u(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// One column, stored and loaded (the load waits).
+__device__ __forceinline__ void tmem_st1_u(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_ld1_u(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r)
+               : "r"(taddr)
+               : "memory");
+  return r;
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// The larger of three, and two fp32 operations in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float b) {   // x = x a + b, ...
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n"
+      " mov.b64 r, {%3, %3};\n fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {   // x += a, y += b
+  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n"
+      " add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
 }
 // 2^x on the SFU (approximate, flush-to-zero; 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {
