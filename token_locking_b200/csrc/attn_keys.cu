@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
     }
     // whole unit of a sequence's full key list: final rows; else partial ones
     const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
-    const size_t slot_f = (size_t)KS_T * (D + 2);
+    const KeyRecs recs(a, KS_T);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * ty + i;
@@ -187,20 +187,12 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
           a.lse[(size_t)row * a.H + h] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * KEY_LN2;
         continue;
       }
-      float *rec;
-      if (whole)
-        rec = a.ws + 2 * (size_t)gridDim.x * slot_f +
-              (((size_t)(b < 0 ? 0 : 1) * a.M + row) * a.H + h) * (D + 2);
-      else
-        rec = a.ws + kp_slot(blockIdx.x, pc.t0) * slot_f + (size_t)r * (D + 2);
+      const size_t rec = whole ? key_rec_row(a, KS_T, b < 0 ? 0 : 1, row, h)
+                               : key_rec_slot(kp_slot(blockIdx.x, pc.t0), KS_T, r);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
-        if (4 * tx + 64 * c < D) {
-          float2 *dst = reinterpret_cast<float2 *>(rec + 2 + 4 * tx + 64 * c);
-          dst[0] = make_float2(acc[i][c].x, acc[i][c].y);
-          dst[1] = make_float2(acc[i][c].z, acc[i][c].w);
-        }
-      if (tx == 0) *reinterpret_cast<float2 *>(rec) = make_float2(m[i], l[i]);
+        if (4 * tx + 64 * c < D) store4(recs.o + rec * D + 4 * tx + 64 * c, acc[i][c]);
+      if (tx == 0) recs.ml[rec] = make_float2(m[i], l[i]);
     }
   }
 }
@@ -218,20 +210,19 @@ struct JoinAcc {
   float4 o;
 };
 
-__device__ __forceinline__ void join_rec(JoinAcc &x, const float *rec, int D, int lane) {
-  const float2 ml = __ldcg(reinterpret_cast<const float2 *>(rec));
+__device__ __forceinline__ void join_rec(JoinAcc &x, const KeyRecs &recs, size_t rec, int lane) {
+  const float2 ml = __ldcg(recs.ml + rec);
   const float mn = fmaxf(x.m, ml.x);
   const float ms = mn == -INFINITY ? 0.f : mn;
   const float ca = exp2f(x.m - ms), cb = exp2f(ml.x - ms);
   x.l = x.l * ca + ml.y * cb;
   x.m = mn;
-  if (4 * lane < D) {
-    const float2 u = __ldcg(reinterpret_cast<const float2 *>(rec + 2 + 4 * lane));
-    const float2 v = __ldcg(reinterpret_cast<const float2 *>(rec + 4 + 4 * lane));
+  if (4 * lane < recs.D) {
+    const float4 u = __ldcg(reinterpret_cast<const float4 *>(recs.o + rec * recs.D + 4 * lane));
     x.o.x = x.o.x * ca + u.x * cb;
     x.o.y = x.o.y * ca + u.y * cb;
-    x.o.z = x.o.z * ca + v.x * cb;
-    x.o.w = x.o.w * ca + v.y * cb;
+    x.o.z = x.o.z * ca + u.z * cb;
+    x.o.w = x.o.w * ca + u.w * cb;
   }
 }
 
@@ -253,19 +244,16 @@ __device__ __forceinline__ void join_unit(const KeyArgs &a, const KeyPlan &pl, J
   const int T = pl.T[j];
   if (T == 0) return;
   const int wu = pl.wbase[j] + (unit * a.Hkv + hk) * (T + KP_OV);
-  const size_t slot_f = (size_t)rt * (a.D + 2);
+  const KeyRecs recs(a, rt);
   const int c1 = (wu + T + KP_OV - 1) / pl.chunk;
   for (int c = wu / pl.chunk; c <= c1; ++c) {
     int t0, t1;
     kp_piece_of(pl, wu, T, c, t0, t1);
     if (t1 <= t0) continue;
-    const float *rec;
-    if (t0 == 0 && t1 == T)
-      rec = a.ws + 2 * (size_t)a.n_ctas * slot_f +
-            (((size_t)(kp_seq(pl, j) < 0 ? 0 : 1) * a.M + row) * a.H + h) * (a.D + 2);
-    else
-      rec = a.ws + kp_slot(c, t0) * slot_f + (size_t)r * (a.D + 2);
-    join_rec(x, rec, a.D, lane);
+    join_rec(x, recs,
+             t0 == 0 && t1 == T ? key_rec_row(a, rt, kp_seq(pl, j) < 0 ? 0 : 1, row, h)
+                                : key_rec_slot(kp_slot(c, t0), rt, r),
+             lane);
   }
 }
 

@@ -426,7 +426,9 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     const uint32_t t_o = tmem_base + ((uint32_t)(quarter * 32) << 16) + C::O_COL + j * D +
                          half * (D / 2);      // this warpgroup's columns of O
     const float c2 = a.scale * KEY_LOG2E;
-    const size_t slot_f = (size_t)2 * QR * a.G * (D + 2);
+    const int rt = 2 * QR * a.G;              // packed rows of a unit
+    const KeyRecs recs(a, rt);
+    const bool o32 = ((uintptr_t)a.o & 31) == 0 && a.ld_o % 16 == 0;
     uint32_t cs = 0;                          // score tiles taken
     // After a wait that ran out the loops go on without waiting (the abort flag
     // ends later waits at once), so that both halves of a tile meet below.
@@ -443,10 +445,13 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       int r0, rn;
       if (rows_of(r0, rn) <= j) continue;
       const int b = kp_seq(pl, pc.job);
+      // the tiles that end the prefix and the sequence's own keys, and their keys
+      const int t_pre = b < 0 || !pl.stacked ? tp - 1 : -1, n_pre = a.prefix_len - (tp - 1) * BN;
+      const int t_own = b < 0 ? -1 : pc.T - 1;
+      const int n_own = b < 0 ? 0 : pl.kl[b] - (pl.stacked ? t_own : t_own - tp) * BN;
       float m = -INFINITY, l = 0.f;
       for (int t = pc.t0; t < pc.t1; ++t, ++cs) {
-        const bool pre = b < 0 || (!pl.stacked && t < tp);
-        const int nv = (pre ? a.prefix_len : pl.kl[b]) - (pre || pl.stacked ? t : t - tp) * BN;
+        const int nv = t == t_pre ? n_pre : t == t_own ? n_own : BN;
         wait(0, cs & 1u);
         tc_fence_after();
         float s[HB];
@@ -526,32 +531,36 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
           tmem_ld_cols<32>(t_o + c0, o);
           if (live) {
-            uint4 *dst = reinterpret_cast<uint4 *>(orow + c0);
+            uint32_t u[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              dst[c] = make_uint4(kc_pack(o[8 * c] * inv, o[8 * c + 1] * inv),
-                                  kc_pack(o[8 * c + 2] * inv, o[8 * c + 3] * inv),
-                                  kc_pack(o[8 * c + 4] * inv, o[8 * c + 5] * inv),
-                                  kc_pack(o[8 * c + 6] * inv, o[8 * c + 7] * inv));
+            for (int c = 0; c < 16; ++c) u[c] = kc_pack(o[2 * c] * inv, o[2 * c + 1] * inv);
+            if (o32) {
+              st_global_v8(orow + c0, u);
+              st_global_v8(orow + c0 + 16, u + 8);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                reinterpret_cast<uint4 *>(orow + c0)[c] =
+                    make_uint4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+            }
           }
         }
         if (live && a.lse && half == 0)
           a.lse[(size_t)row * a.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * KEY_LN2;
       } else {
-        float *rec = whole ? a.ws + 2 * (size_t)gridDim.x * slot_f +
-                                 (((size_t)(b < 0 ? 0 : 1) * a.M + row) * a.H + h) * (D + 2)
-                           : a.ws + kp_slot(blockIdx.x, pc.t0) * slot_f +
-                                 (size_t)(j * QR * a.G + r) * (D + 2);
+        const size_t rec = whole ? key_rec_row(a, rt, b < 0 ? 0 : 1, row, h)
+                                 : key_rec_slot(kp_slot(blockIdx.x, pc.t0), rt, j * QR * a.G + r);
+        float *dst = recs.o + rec * D + half * (D / 2);
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
           tmem_ld_cols<32>(t_o + c0, o);
           if (live) {
-            float2 *dst = reinterpret_cast<float2 *>(rec + 2 + half * (D / 2) + c0);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) dst[c] = make_float2(o[2 * c], o[2 * c + 1]);
+            for (int c = 0; c < 32; c += 8)
+              st_global_v8(dst + c0 + c, reinterpret_cast<const uint32_t *>(o + c));
           }
         }
-        if (live && half == 0) *reinterpret_cast<float2 *>(rec) = make_float2(m, l);
+        if (live && half == 0) recs.ml[rec] = make_float2(m, l);
       }
     }
   }

@@ -234,7 +234,8 @@ cudaError_t key_attn_tc_setup(int D);
 // Most CTAs a launch of this head layout uses, and the workspace for it.
 int key_attn_ctas(int dtype, int D, int num_sms);
 int key_mass_ctas(int dtype, int D, int G, int num_sms);
-// [2 nC slots][rows][D + 2] partial rows, then (stacked) [2][rows][H][D + 2].
+// D + 2 floats for each of 2 n_ctas slots' partial rows and, for up to stack_rows
+// rows whose prefix is a job of its own, two per row and head.
 size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows);
 size_t key_mass_ws_floats(int dtype, int D, int G, int batch, int n_ctx, int n_ctas);
 cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s);

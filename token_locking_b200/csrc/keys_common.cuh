@@ -35,4 +35,25 @@ __device__ __forceinline__ int key_pos(const KeyArgs &a, int b, int i) {
   return -1;
 }
 
+// Partial rows (maximum in base 2, sum, unnormalised o): two slots of rt packed
+// rows per CTA for units that a share cut, then (with a joint prefix) one per
+// row, head and part.  All o rows come first, then all (maximum, sum) pairs.
+struct KeyRecs {
+  float *o;
+  float2 *ml;
+  int D;
+  __device__ __forceinline__ KeyRecs(const KeyArgs &a, int rt) {
+    const size_t n = 2 * (size_t)a.n_ctas * rt + (a.stack ? 2 * (size_t)a.M * a.H : 0);
+    o = a.ws;
+    ml = reinterpret_cast<float2 *>(a.ws + n * a.D);
+    D = a.D;
+  }
+};
+__device__ __forceinline__ size_t key_rec_slot(int slot, int rt, int r) {
+  return (size_t)slot * rt + r;
+}
+__device__ __forceinline__ size_t key_rec_row(const KeyArgs &a, int rt, int part, int row, int h) {
+  return 2 * (size_t)a.n_ctas * rt + ((size_t)part * a.M + row) * a.H + h;
+}
+
 }  // namespace sl

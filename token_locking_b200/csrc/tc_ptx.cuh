@@ -288,6 +288,12 @@ __device__ __forceinline__ uint32_t tmem_ld1_u(uint32_t taddr) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// 32 bytes (32-byte aligned) in one store: a whole sector per lane.
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // The larger of three, and two fp32 operations in one instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
