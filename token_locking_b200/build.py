@@ -20,10 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsurelock.so")
 SOURCES = ["api.cu", "layers.cu", "lock.cu", "attn.cu", "attn_tc.cu", "gemm_tc.cu",
-           "attn_keys.cu", "attn_keys_tc.cu", "attn_mass.cu", "evict.cu", "api_keys.cu"]
+           "attn_keys.cu", "attn_keys_tc.cu", "attn_mass.cu", "attn_mass_tc.cu", "evict.cu", "api_keys.cu"]
 HEADERS = [os.path.join(CSRC, "common.cuh"), os.path.join(CSRC, "internal.h"),
            os.path.join(CSRC, "tc_ptx.cuh"), os.path.join(CSRC, "keys_plan.cuh"),
-           os.path.join(CSRC, "keys_common.cuh"),
+           os.path.join(CSRC, "keys_common.cuh"), os.path.join(CSRC, "keys_tc.cuh"),
            os.path.join(INCLUDE, "surelock.h")]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",

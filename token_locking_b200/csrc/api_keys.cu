@@ -122,14 +122,14 @@ extern "C" sl_status sl_key_attn_create(const sl_key_attn_config *cfg, sl_key_at
     return cuda_fail(e, "sl_key_attn_create");
   }
   a->attn_ctas = key_attn_ctas(cfg->dtype, cfg->head_dim, a->num_sms);
-  a->mass_ctas = key_mass_ctas(cfg->dtype, cfg->head_dim, group, a->num_sms);
+  a->mass_ctas = key_mass_ctas(cfg->dtype, cfg->head_dim, a->num_sms);
   // a joint pass over the prefix pays while a sequence's rows leave most of a
   // 128-row tile empty; above that the workspace for it is not reserved
   a->stack_rows =
       cfg->prefix ? (int)std::min<long long>(cfg->max_rows, (long long)96 * cfg->batch / group) : 0;
   const size_t floats = std::max(
       key_attn_ws_floats(cfg->dtype, cfg->head_dim, cfg->n_heads, a->attn_ctas, a->stack_rows),
-      key_mass_ws_floats(cfg->dtype, cfg->head_dim, group, cfg->batch, cfg->n_ctx, a->mass_ctas));
+      key_mass_ws_floats(cfg->dtype, cfg->head_dim, cfg->batch, cfg->n_ctx, a->mass_ctas));
   a->err = device_error_word();
   if (!a->err || cudaMalloc((void **)&a->ws, floats * sizeof(float)) != cudaSuccess) {
     cudaGetLastError();

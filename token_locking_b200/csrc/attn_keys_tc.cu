@@ -34,7 +34,7 @@
 #include "common.cuh"
 #include "keys_common.cuh"
 #include "keys_plan.cuh"
-#include "tc_ptx.cuh"
+#include "keys_tc.cuh"
 
 namespace sl {
 
@@ -79,68 +79,9 @@ struct KcParams {
   KeyArgs a;
 };
 
-// N fp32 columns of this thread's TMEM lane (N a multiple of 8), one wait.
-template <int N> __device__ __forceinline__ void tmem_ld_cols(uint32_t t, float *s) {
-#pragma unroll
-  for (int c = 0; c + 32 <= N; c += 32) tmem_ld32_nw(t + c, s + c);
-  if constexpr (N % 32 >= 16) tmem_ld16_nw(t + N / 32 * 32, s + N / 32 * 32);
-  if constexpr (N % 16 == 8) tmem_ld8_nw(t + N - 8, s + N - 8);
-  tmem_wait_ld();
-}
-// N columns of it (N a multiple of 4), without a wait.
-template <int N> __device__ __forceinline__ void tmem_st_cols(uint32_t t, const uint32_t *r) {
-  static_assert(N < 32 && N % 4 == 0, "columns");
-  if constexpr (N >= 16) tmem_st16_u(t, r);
-  if constexpr (N % 16 >= 8) tmem_st8_u(t + N / 16 * 16, r + N / 16 * 16);
-  if constexpr (N % 8 == 4) tmem_st4_u(t + N - 4, r + N - 4);
-}
-// The largest of s[0..N) (N even).
-template <int N> __device__ __forceinline__ float max_of(const float *s) {
-  float a = s[0], b = s[1];
-#pragma unroll
-  for (int i = 2; i + 3 < N; i += 4) {
-    a = max3(a, s[i], s[i + 1]);
-    b = max3(b, s[i + 2], s[i + 3]);
-  }
-  if constexpr (N % 4 == 0) a = max3(a, s[N - 2], s[N - 1]);
-  return fmaxf(a, b);
-}
-
 __device__ __forceinline__ uint32_t kc_pack(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
-}
-
-// All lanes wait; the outcome is the same for all.  The waiting loop is kept out
-// of line: the roles' code competes for the instruction caches.
-__device__ __noinline__ bool kc_wait_long(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          unsigned long long lim) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, lim));
-}
-__device__ __forceinline__ bool kc_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                        unsigned long long lim) {
-  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-  return kc_wait_long(bar, parity, abort_flag, lim);
-}
-
-// One lane of the warp (the same every time).
-__device__ __forceinline__ bool kc_elect() {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
-               : "=r"(ok));
-  return ok != 0;
-}
-// 16 bytes to shared memory, zeros where the source is not there.
-__device__ __forceinline__ void kc_copy16(uint32_t dst, const void *src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void kc_copy_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N> __device__ __forceinline__ void kc_copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int D, int BN>
@@ -237,7 +178,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       };
       int nxt = entry(pc.t0, my_row), nxt2 = entry(pc.t0, my_row2);
       if (pw == 0) {
-        if (!kc_wait(bar(C::B_QE), (uint32_t)(np & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
+        if (!key_wait(bar(C::B_QE), (uint32_t)(np & 1) ^ 1u, abort_flag, lim)) { ok = false; break; }
         if (lane == 0) {
           mbar_expect_tx(bar(C::B_QF), (uint32_t)(nj * C::NB * 128 * a.G * QR));
           for (int j = 0; j < nj; ++j)
@@ -266,10 +207,10 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         nxt2 = entry(t + 1, my_row2);
         const uint32_t dst = sbase + C::KV_OFF + 2 * st * C::SLOT;
         if (!by_row && pend > 0) {
-          kc_copy_wait<0>();
+          key_copy_wait<0>();
           while (pend > 0) hand_over();
         }
-        if (!kc_wait(bar(C::B_E + st), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
+        if (!key_wait(bar(C::B_E + st), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
         if (by_row) {
           const long long base = (long long)b * a.n_ctx * a.ld_kv + pc.hk * D + ch * 8;
 #pragma unroll
@@ -281,13 +222,13 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
               const int ps = i * C::RPI < 32
                                  ? __shfl_sync(0xffffffffu, pos, (i * C::RPI + g0) & 31)
                                  : __shfl_sync(0xffffffffu, pos2, (i * C::RPI + g0) & 31);
-              kc_copy16(d0 + i * 2 * C::RPI * 128 + ((i * 2 * C::RPI) & 4 ? sw1 : sw0),
+              key_copy16(d0 + i * 2 * C::RPI * 128 + ((i * 2 * C::RPI) & 4 ? sw1 : sw0),
                         src + (ps < 0 ? 0 : ps) * a.ld_kv, ps >= 0);
             }
           }
-          kc_copy_commit();
+          key_copy_commit();
           if (++pend == C::LAG) {
-            kc_copy_wait<C::LAG - 1>();
+            key_copy_wait<C::LAG - 1>();
             hand_over();
           }
         } else {
@@ -316,11 +257,11 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       }
       if (!ok) break;
       if (pend > 0) {
-        kc_copy_wait<0>();
+        key_copy_wait<0>();
         while (pend > 0) hand_over();
       }
     }
-    kc_copy_wait<0>();
+    key_copy_wait<0>();
     if (!ok && lane == 0) {
       atomicExch(a.err, DEV_TIMEOUT_PRODUCER);
       *abort_flag = 1;
@@ -339,7 +280,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     const int j = warp - 1;                   // row tile
     constexpr uint32_t id_s = idesc_bf16_f32<BN>();
     constexpr uint32_t id_o = idesc_bf16_f32_bmn<D>();
-    const bool leader = kc_elect();
+    const bool leader = key_elect();
     const uint64_t dq = smem_desc_sw128(sbase + j * C::NB * C::QBOX);
     const uint64_t dk = smem_desc_sw128(sbase + C::KV_OFF);
     const uint64_t dv = smem_desc_sw128_mn(sbase + C::KV_OFF + C::SLOT, C::KBOX, 1024);
@@ -353,16 +294,16 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       int r0, rn;
       const bool mine = j < rows_of(r0, rn);
       const int nt = pc.t1 - pc.t0;
-      ok = kc_wait(bar(C::B_QF), (uint32_t)(np & 1), abort_flag, lim);
+      ok = key_wait(bar(C::B_QF), (uint32_t)(np & 1), abort_flag, lim);
       ++np;
       // scores of tile t are issued one tile ahead of its P V product
       for (int t = -1; ok && t < nt; ++t) {
         if (t + 1 < nt) {
-          ok = kc_wait(bar(C::B_F + ks), kph, abort_flag, lim);
+          ok = key_wait(bar(C::B_F + ks), kph, abort_flag, lim);
           if (!ok) break;
           if (mine) {
             // the buffer's last scores have been read
-            ok = kc_wait(tbar(j, 1), cs ^ 1u, abort_flag, lim);
+            ok = key_wait(tbar(j, 1), cs ^ 1u, abort_flag, lim);
             if (!ok) break;
             tc_fence_after();
             const uint64_t bk = dk + (uint64_t)(uint32_t)(ks * (2 * C::SLOT >> 4));
@@ -384,7 +325,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         }
         if (t < 0) continue;
         if (mine) {
-          ok = kc_wait(tbar(j, 2), cv, abort_flag, lim);
+          ok = key_wait(tbar(j, 2), cv, abort_flag, lim);
           if (!ok) break;
           tc_fence_after();
           const uint64_t bv = dv + (uint64_t)(uint32_t)(vs * (2 * C::SLOT >> 4));
@@ -435,7 +376,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     bool ok = true;
     auto wait = [&](int k, uint32_t parity) {
       if (!ok) return;
-      ok = kc_wait(tbar(j, k), parity, abort_flag, lim);
+      ok = key_wait(tbar(j, k), parity, abort_flag, lim);
       if (!ok && lane == 0) {
         atomicExch(a.err, DEV_TIMEOUT_EPI);
         *abort_flag = 1;

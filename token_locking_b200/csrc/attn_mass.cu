@@ -22,13 +22,6 @@ constexpr int MS_T = 64;
 constexpr int MS_THREADS = 256;
 }  // namespace
 
-// mass = decay mass_prev at every position, before the weights are added
-__device__ __forceinline__ void mass_start(const KeyArgs &a, int i, int n_threads) {
-  const long long n = (long long)a.batch * a.n_ctx;
-  for (long long e = i; e < n; e += n_threads)
-    a.mass[e] = a.decay == 0.f ? 0.f : a.decay * a.mass_prev[e];
-}
-
 // 64 keys against 64 packed rows (qr, g) at a time in fp32 arithmetic; thread
 // (ty, tx) of 16 x 16 holds the scores of rows 4 ty + i and keys tx + 16 j.
 template <typename T>
@@ -43,7 +36,7 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   const int QR = MS_T / a.G;
   pdl_wait();
   if (tid < 32) key_plan_build(pl, a, QR, MS_T, gridDim.x, true, lane);
-  mass_start(a, blockIdx.x * MS_THREADS + tid, gridDim.x * MS_THREADS);
+  key_mass_start(a, blockIdx.x * MS_THREADS + tid, gridDim.x * MS_THREADS);
   __syncthreads();
   pdl_trigger();
   const float c2 = a.scale * KEY_LOG2E;
@@ -132,10 +125,12 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   }
 }
 
-// Adds each key's weight: one thread per entry of a key set.  An entry that a
-// list names twice counts twice, so the additions are atomic; otherwise each
-// position receives one addition and the result does not depend on any order.
-__global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int uq, int kt) {
+// Adds each key's weight (`parts` sums of it): one thread per entry of a key
+// set.  An entry that a list names twice counts twice, so the additions are
+// atomic; a position that is named once receives one addition, and its result
+// does not depend on any order.
+__global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int uq, int kt,
+                                                           int parts) {
   __shared__ KeyPlan pl;
   pdl_wait();
   pdl_trigger();
@@ -152,9 +147,11 @@ __global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int 
       int t0, t1;
       kp_piece_of(pl, wu, T, c, t0, t1);
       if (t1 <= t0) continue;
-      v += t0 == 0 && t1 == T
-               ? __ldcg(a.ws + 2 * (size_t)a.n_ctas * kt + (size_t)b * a.n_ctx + i)
-               : __ldcg(a.ws + (size_t)kp_slot(c, t0) * kt + i % kt);
+      for (int q = 0; q < parts; ++q)
+        v += t0 == 0 && t1 == T
+                 ? __ldcg(a.ws + 2 * (size_t)a.n_ctas * parts * kt +
+                          ((size_t)q * a.batch + b) * a.n_ctx + i)
+                 : __ldcg(a.ws + ((size_t)kp_slot(c, t0) * parts + q) * kt + i % kt);
     }
     const int pos = key_pos(a, b, i);
     if (pos >= 0) atomicAdd(a.mass + (size_t)b * a.n_ctx + pos, v);
@@ -169,33 +166,35 @@ template <typename T> cudaError_t run_mass_simt(const KeyArgs &a, cudaStream_t s
   const cudaError_t e =
       launch_k(key_mass_simt_kernel<T>, a.n_ctas, MS_THREADS, mass_simt_smem(a.D), s, a);
   if (e != cudaSuccess) return e;
-  const dim3 grid(std::min((a.n_ctx + 255) / 256, 256), a.batch);
-  return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, MS_T / a.G, MS_T);
+  return launch_key_mass_add(a, MS_T / a.G, MS_T, 1, s);
 }
 }  // namespace
 
 cudaError_t key_mass_setup(int dtype, int D) {
+  if (key_attn_tc_takes(dtype, D)) return key_mass_tc_setup(D);
   const int smem = (int)mass_simt_smem(D);
   const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
   return dtype == SL_BF16 ? cudaFuncSetAttribute(key_mass_simt_kernel<bf16>, attr, smem)
                           : cudaFuncSetAttribute(key_mass_simt_kernel<float>, attr, smem);
 }
 
-int key_mass_ctas(int dtype, int D, int G, int num_sms) {
-  (void)dtype;
-  (void)D;
-  (void)G;
-  return num_sms * 2;
+int key_mass_ctas(int dtype, int D, int num_sms) {
+  return num_sms * (key_attn_tc_takes(dtype, D) ? 1 : 2);
 }
 
-size_t key_mass_ws_floats(int dtype, int D, int G, int batch, int n_ctx, int n_ctas) {
-  (void)dtype;
-  (void)D;
-  (void)G;
-  return 2 * (size_t)n_ctas * MS_T + (size_t)batch * n_ctx;
+size_t key_mass_ws_floats(int dtype, int D, int batch, int n_ctx, int n_ctas) {
+  const bool tc = key_attn_tc_takes(dtype, D);
+  const size_t slot = tc ? 2 * 256 : MS_T, parts = tc ? 2 : 1;
+  return 2 * (size_t)n_ctas * slot + parts * batch * n_ctx;
+}
+
+cudaError_t launch_key_mass_add(const KeyArgs &a, int uq, int kt, int parts, cudaStream_t s) {
+  const dim3 grid(std::min((a.n_ctx + 255) / 256, 256), a.batch);
+  return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, uq, kt, parts);
 }
 
 cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s) {
+  if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_mass_tc(a, s);
   return a.dtype == SL_BF16 ? run_mass_simt<bf16>(a, s) : run_mass_simt<float>(a, s);
 }
 

@@ -233,16 +233,21 @@ cudaError_t key_mass_setup(int dtype, int D);
 cudaError_t key_attn_tc_setup(int D);
 // Most CTAs a launch of this head layout uses, and the workspace for it.
 int key_attn_ctas(int dtype, int D, int num_sms);
-int key_mass_ctas(int dtype, int D, int G, int num_sms);
+int key_mass_ctas(int dtype, int D, int num_sms);
 // D + 2 floats for each of 2 n_ctas slots' partial rows and, for up to stack_rows
 // rows whose prefix is a job of its own, two per row and head.
 size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows);
-size_t key_mass_ws_floats(int dtype, int D, int G, int batch, int n_ctx, int n_ctas);
+size_t key_mass_ws_floats(int dtype, int D, int batch, int n_ctx, int n_ctas);
 cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s);
 cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s);
 // bf16 heads of 64 and 128 on the tensor cores (attn_keys_tc.cu)
 bool key_attn_tc_takes(int dtype, int D);
 cudaError_t launch_key_attn_tc(const KeyArgs &a, cudaStream_t s);
+cudaError_t key_mass_tc_setup(int D);
+cudaError_t launch_key_mass_tc(const KeyArgs &a, cudaStream_t s);
+// Adds the weights that a weight kernel left: units of kt keys, blocks of uq
+// query rows, `parts` sums a key.
+cudaError_t launch_key_mass_add(const KeyArgs &a, int uq, int kt, int parts, cudaStream_t s);
 // Joins partial rows: slots of rt packed rows, units of uq query rows, tiles of kt keys.
 cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, int kt, cudaStream_t s);
 

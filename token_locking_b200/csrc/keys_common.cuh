@@ -35,6 +35,13 @@ __device__ __forceinline__ int key_pos(const KeyArgs &a, int b, int i) {
   return -1;
 }
 
+// mass = decay mass_prev at every position, before the weights are added.
+__device__ __forceinline__ void key_mass_start(const KeyArgs &a, int i, int n_threads) {
+  const long long n = (long long)a.batch * a.n_ctx;
+  for (long long e = i; e < n; e += n_threads)
+    a.mass[e] = a.decay == 0.f ? 0.f : a.decay * a.mass_prev[e];
+}
+
 // Partial rows (maximum in base 2, sum, unnormalised o): two slots of rt packed
 // rows per CTA for units that a share cut, then (with a joint prefix) one per
 // row, head and part.  All o rows come first, then all (maximum, sum) pairs.

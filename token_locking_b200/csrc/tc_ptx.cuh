@@ -306,6 +306,12 @@ __device__ __forceinline__ void fma2(float &x, float &y, float a, float b) {   /
       : "+f"(x), "+f"(y)
       : "f"(a), "f"(b));
 }
+__device__ __forceinline__ void fma2v(float &x, float &y, float a, float b, float c) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n"       // x = x a + b
+      " mov.b64 r, {%3, %4};\n fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}\n"   // y = y a + c
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c));
+}
 __device__ __forceinline__ void add2(float &x, float &y, float a, float b) {   // x += a, y += b
   asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n"
       " add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}\n"
