@@ -283,7 +283,7 @@ def _check_evict(got, want, N):
 
 
 @pytest.mark.parametrize("B,N", [(1, 1), (2, 31), (3, 1024), (1, 1025), (64, 300), (2, 5000),
-                                 (2, 40000), (1, 131073)])
+                                 (2, 40000), (1, 131073), (1, 500001)])
 @pytest.mark.parametrize("kind", ["heavy", "ties", "zeros", "odd"])
 def test_evict_matches_sorting(cuda_dev, B, N, kind):
     rng = np.random.default_rng(N + B)
