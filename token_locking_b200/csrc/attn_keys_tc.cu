@@ -8,7 +8,7 @@
 //                [G heads][64], so that packed rows land in order whatever G,
 //                and every full tile of the prefix or of an unlisted cache.
 //                Listed keys, and the tile a key set ends in, are copied row by
-//                row by both warps (16-byte asynchronous copies, three tiles
+//                row by both warps (16-byte asynchronous copies, two tiles
 //                in flight), zeros for entries that are not there: what lies
 //                behind a key set never reaches shared memory.  (Four-row TMA
 //                gathers instead took 17 clocks a row of 128 bytes, 7200 clocks
@@ -58,7 +58,7 @@ template <int D, int BN> struct KcCfg {
   static constexpr int B_DRAIN = B_TILE + 8, B_COUNT = B_DRAIN + 2;
   // row copies: 16-byte chunks of a row, rows of a warp instruction, instructions
   // of each of the two warps, tiles in flight
-  static constexpr int CH = D / 8, RPI = 32 / CH, NI = BN / RPI / 2, LAG = 3;
+  static constexpr int CH = D / 8, RPI = 32 / CH, NI = BN / RPI / 2, LAG = 2;
   static constexpr int PLAN_OFF = BAR_OFF + 512;
   // TMEM columns: per row tile S, then P (two bf16 keys a column), from a
   // multiple of 64; then O of both
