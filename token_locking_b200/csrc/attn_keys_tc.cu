@@ -17,13 +17,14 @@
 //                j (warp 1 owns TMEM).  One issuing warp for both tiles took
 //                some 2500 clocks a tile of keys, in waits and issue alone.
 //   warps 4..19  softmax: two warpgroups per row tile, a row per thread in
-//                each and half of the tile's keys; both take the maximum over
-//                all of them, so they need not meet but at the end, for the row's
-//                sum.  (One warpgroup per tile, all keys: 2300 clocks per 80 keys,
-//                with two warps per scheduler too few to keep the exponentials
-//                running through the waits.)  The maximum is raised only when a
-//                tile exceeds it by 2^8 (O is rescaled then); p is rounded to
-//                bf16 for the product (half a step), its sum taken in fp32 before.
+//                each and half of the tile's keys; the halves exchange their
+//                maxima through TMEM.  (One warpgroup per tile, all keys: 2300
+//                clocks per 80 keys, with two warps per scheduler too few to keep
+//                the exponentials running through the waits.  Both halves taking
+//                the maximum over all keys: 2 % more time.)  The maximum is
+//                raised only when a tile exceeds it by 2^8 (O is rescaled then);
+//                p is rounded to bf16 for the product (half a step), its sum taken
+//                in fp32 before.
 // The two row tiles are two independent chains (scores, softmax, P V) that
 // share K and V, so that the tensor cores work on one while the other's
 // exponentials are taken.
@@ -64,7 +65,8 @@ template <int D, int BN> struct KcCfg {
   // multiple of 64; then O of both
   static constexpr uint32_t T_COLS = (BN + BN / 2 + 63) / 64 * 64;
   static constexpr uint32_t O_COL = 2 * T_COLS;
-  static constexpr uint32_t L_COL = BN + BN / 2;        // the two halves' row sums
+  static constexpr uint32_t X_COL = BN + BN / 2;        // the two halves' row maxima, twice
+  static constexpr uint32_t L_COL = X_COL + 4;          // and row sums
   static_assert(O_COL + 2 * D <= 512 && L_COL + 2 <= T_COLS, "TMEM columns");
   static constexpr int HB = BN / 2;                     // keys of a softmax warpgroup
   static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
@@ -396,13 +398,6 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         wait(0, cs & 1u);
         tc_fence_after();
         float s[HB];
-        // the other half's keys for the maximum, then this one's
-        tmem_ld_cols<HB>(t_row + (half ^ 1) * HB, s);
-        if (nv < BN) {
-#pragma unroll
-          for (int i = 0; i < HB; ++i) s[i] = (half ^ 1) * HB + i < nv ? s[i] : -INFINITY;
-        }
-        float mt = max_of<HB>(s);
         tmem_ld_cols<HB>(t_s, s);
         tc_fence_before();
         __syncwarp();
@@ -411,7 +406,16 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
 #pragma unroll
           for (int i = 0; i < HB; ++i) s[i] = half * HB + i < nv ? s[i] : -INFINITY;
         }
-        mt = c2 * fmaxf(mt, max_of<HB>(s));
+        // the row's maximum over both halves, through two columns of TMEM (the
+        // other two of four next time: the barrier orders the rest)
+        float mt = max_of<HB>(s);
+        const uint32_t t_x = t_row + C::X_COL + 2 * (cs & 1u);
+        tmem_st1_u(t_x + half, __float_as_uint(mt));
+        tmem_wait_st();
+        tc_fence_before();
+        named_bar_sync(1 + j * 4 + quarter, 64);
+        tc_fence_after();
+        mt = c2 * fmaxf(mt, __uint_as_float(tmem_ld1_u(t_x + (half ^ 1))));
         const bool first = t == pc.t0;
         const float m_new = fmaxf(m, mt);
         const bool resc = !first && m_new > m + KC_RESCALE;
