@@ -75,7 +75,8 @@ sl_status fill_args(const sl_key_attn *a, const char *fn, int rows, const void *
   x->seq_off = set->d_seq_off;
   x->key_len = set->d_key_len;
   x->keys = set->d_keys;
-  x->ws = a->ws;
+  x->plan = reinterpret_cast<int *>(a->ws);
+  x->ws = a->ws + KEY_PLAN_WORDS;
   x->err = a->err;
   x->wait_ns = wait_limit_ns() ? wait_limit_ns() : WAIT_LIMIT_NS;
   return SL_OK;
@@ -131,7 +132,7 @@ extern "C" sl_status sl_key_attn_create(const sl_key_attn_config *cfg, sl_key_at
       key_attn_ws_floats(cfg->dtype, cfg->head_dim, cfg->n_heads, a->attn_ctas, a->stack_rows),
       key_mass_ws_floats(cfg->dtype, cfg->head_dim, cfg->batch, cfg->n_ctx, a->mass_ctas));
   a->err = device_error_word();
-  if (!a->err || cudaMalloc((void **)&a->ws, floats * sizeof(float)) != cudaSuccess) {
+  if (!a->err || cudaMalloc((void **)&a->ws, (floats + KEY_PLAN_WORDS) * sizeof(float)) != cudaSuccess) {
     cudaGetLastError();
     sl_key_attn_destroy(a);
     return fail(SL_ERR_OOM, "sl_key_attn_create: device allocation failed");

@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
   pdl_wait();
   if (tid < 32) key_plan_build(pl, a, QR, KS_T, gridDim.x, false, lane);
   __syncthreads();
+  if (blockIdx.x == 0) key_plan_publish(pl, a.plan, tid, KS_THREADS);
   pdl_trigger();
   const int tp = kp_tiles(a.prefix_len, KS_T);
   const int d4 = D >> 2;
@@ -210,20 +211,16 @@ struct JoinAcc {
   float4 o;
 };
 
-__device__ __forceinline__ void join_rec(JoinAcc &x, const KeyRecs &recs, size_t rec, int lane) {
-  const float2 ml = __ldcg(recs.ml + rec);
+__device__ __forceinline__ void join_rec(JoinAcc &x, float2 ml, float4 u) {
   const float mn = fmaxf(x.m, ml.x);
   const float ms = mn == -INFINITY ? 0.f : mn;
   const float ca = exp2f(x.m - ms), cb = exp2f(ml.x - ms);
   x.l = x.l * ca + ml.y * cb;
   x.m = mn;
-  if (4 * lane < recs.D) {
-    const float4 u = __ldcg(reinterpret_cast<const float4 *>(recs.o + rec * recs.D + 4 * lane));
-    x.o.x = x.o.x * ca + u.x * cb;
-    x.o.y = x.o.y * ca + u.y * cb;
-    x.o.z = x.o.z * ca + u.z * cb;
-    x.o.w = x.o.w * ca + u.w * cb;
-  }
+  x.o.x = x.o.x * ca + u.x * cb;
+  x.o.y = x.o.y * ca + u.y * cb;
+  x.o.z = x.o.z * ca + u.z * cb;
+  x.o.w = x.o.w * ca + u.w * cb;
 }
 
 template <typename T>
@@ -246,24 +243,38 @@ __device__ __forceinline__ void join_unit(const KeyArgs &a, const KeyPlan &pl, J
   const int wu = pl.wbase[j] + (unit * a.Hkv + hk) * (T + KP_OV);
   const KeyRecs recs(a, rt);
   const int c1 = (wu + T + KP_OV - 1) / pl.chunk;
-  for (int c = wu / pl.chunk; c <= c1; ++c) {
-    int t0, t1;
-    kp_piece_of(pl, wu, T, c, t0, t1);
-    if (t1 <= t0) continue;
-    join_rec(x, recs,
-             t0 == 0 && t1 == T ? key_rec_row(a, rt, kp_seq(pl, j) < 0 ? 0 : 1, row, h)
-                                : key_rec_slot(kp_slot(c, t0), rt, r),
-             lane);
+  constexpr int U = 2;                                 // pieces whose loads are in flight together
+  for (int c = wu / pl.chunk; c <= c1; c += U) {
+    float2 ml[U];
+    float4 u[U];
+    bool on[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      int t0 = 0, t1 = 0;
+      if (c + e <= c1) kp_piece_of(pl, wu, T, c + e, t0, t1);
+      on[e] = t1 > t0;
+      if (on[e]) {
+        const size_t rec = t0 == 0 && t1 == T
+                               ? key_rec_row(a, rt, kp_seq(pl, j) < 0 ? 0 : 1, row, h)
+                               : key_rec_slot(kp_slot(c + e, t0), rt, r);
+        ml[e] = __ldcg(recs.ml + rec);
+        if (4 * lane < a.D)
+          u[e] = __ldcg(reinterpret_cast<const float4 *>(recs.o + rec * a.D + 4 * lane));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e)
+      if (on[e]) join_rec(x, ml[e], u[e]);
   }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) key_join_kernel(const KeyArgs a, int rt, int uq, int kt) {
+__global__ void __launch_bounds__(256, 4) key_join_kernel(const KeyArgs a, int rt, int uq) {
   __shared__ KeyPlan pl;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) key_plan_build(pl, a, uq, kt, a.n_ctas, false, lane);
+  key_plan_fetch(pl, a.plan, threadIdx.x, 256);
   __syncthreads();
   const int W = pl.wbase[pl.njobs];
   const int n_warps = gridDim.x * gridDim.y * 8;
@@ -326,7 +337,7 @@ template <typename T> cudaError_t run_simt(const KeyArgs &a, cudaStream_t s) {
   const cudaError_t e =
       launch_k(key_attn_simt_kernel<T>, a.n_ctas, KS_THREADS, simt_smem(a.D), s, a);
   if (e != cudaSuccess) return e;
-  return launch_key_join(a, KS_T, KS_T / a.G, KS_T, s);
+  return launch_key_join(a, KS_T, KS_T / a.G, s);
 }
 }  // namespace
 
@@ -348,10 +359,10 @@ size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows) {
   return 2 * (size_t)n_ctas * slot_rows * (D + 2) + 2 * (size_t)stack_rows * H * (D + 2);
 }
 
-cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, int kt, cudaStream_t s) {
+cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, cudaStream_t s) {
   const dim3 grid(a.n_ctas, 8);
-  return a.dtype == SL_BF16 ? launch_k(key_join_kernel<bf16>, grid, 256, 0, s, a, rt, uq, kt)
-                            : launch_k(key_join_kernel<float>, grid, 256, 0, s, a, rt, uq, kt);
+  return a.dtype == SL_BF16 ? launch_k(key_join_kernel<bf16>, grid, 256, 0, s, a, rt, uq)
+                            : launch_k(key_join_kernel<float>, grid, 256, 0, s, a, rt, uq);
 }
 
 cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s) {

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
+  if (blockIdx.x == 0) key_plan_publish(pl, a.plan, threadIdx.x, KC_THREADS);
   const uint32_t tmem_base = *tmem_slot;
   const int tp = kp_tiles(a.prefix_len, BN);
 
@@ -544,7 +545,7 @@ template <int D> cudaError_t run_tc(const KeyArgs &a, cudaStream_t s) {
   if (!ok) return cudaErrorInvalidValue;
   const cudaError_t e = launch_k(key_attn_tc_kernel<D, BN>, a.n_ctas, KC_THREADS, C::SMEM, s, p);
   if (e != cudaSuccess) return e;
-  return launch_key_join(a, 2 * QR * a.G, 2 * QR, BN, s);
+  return launch_key_join(a, 2 * QR * a.G, 2 * QR, s);
 }
 }  // namespace
 

@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   if (tid < 32) key_plan_build(pl, a, QR, MS_T, gridDim.x, true, lane);
   key_mass_start(a, blockIdx.x * MS_THREADS + tid, gridDim.x * MS_THREADS);
   __syncthreads();
+  if (blockIdx.x == 0) key_plan_publish(pl, a.plan, tid, MS_THREADS);
   pdl_trigger();
   const float c2 = a.scale * KEY_LOG2E;
   int w = min((long long)blockIdx.x * pl.chunk, (long long)pl.wbase[pl.njobs]), job = 0;
@@ -129,12 +130,11 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
 // set.  An entry that a list names twice counts twice, so the additions are
 // atomic; a position that is named once receives one addition, and its result
 // does not depend on any order.
-__global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int uq, int kt,
-                                                           int parts) {
+__global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int kt, int parts) {
   __shared__ KeyPlan pl;
   pdl_wait();
   pdl_trigger();
-  if (threadIdx.x < 32) key_plan_build(pl, a, uq, kt, a.n_ctas, true, threadIdx.x);
+  key_plan_fetch(pl, a.plan, threadIdx.x, 256);
   __syncthreads();
   const int b = blockIdx.y;
   const int T = pl.T[b];
@@ -166,7 +166,7 @@ template <typename T> cudaError_t run_mass_simt(const KeyArgs &a, cudaStream_t s
   const cudaError_t e =
       launch_k(key_mass_simt_kernel<T>, a.n_ctas, MS_THREADS, mass_simt_smem(a.D), s, a);
   if (e != cudaSuccess) return e;
-  return launch_key_mass_add(a, MS_T / a.G, MS_T, 1, s);
+  return launch_key_mass_add(a, MS_T, 1, s);
 }
 }  // namespace
 
@@ -188,9 +188,9 @@ size_t key_mass_ws_floats(int dtype, int D, int batch, int n_ctx, int n_ctas) {
   return 2 * (size_t)n_ctas * slot + parts * batch * n_ctx;
 }
 
-cudaError_t launch_key_mass_add(const KeyArgs &a, int uq, int kt, int parts, cudaStream_t s) {
+cudaError_t launch_key_mass_add(const KeyArgs &a, int kt, int parts, cudaStream_t s) {
   const dim3 grid(std::min((a.n_ctx + 255) / 256, 256), a.batch);
-  return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, uq, kt, parts);
+  return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, kt, parts);
 }
 
 cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s) {

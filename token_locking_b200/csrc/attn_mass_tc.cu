@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
   __syncthreads();
   tc_fence_after();
   pdl_trigger();
+  if (blockIdx.x == 0) key_plan_publish(pl, a.plan, threadIdx.x, KM_THREADS);
   const uint32_t tmem_base = *tmem_slot;
 
   // every role walks the same pieces, and in them the same (K/V head, block)s
@@ -393,7 +394,7 @@ template <int D> cudaError_t run_mass_tc(const KeyArgs &a, cudaStream_t s) {
   const cudaError_t e =
       launch_k(key_mass_tc_kernel<D>, a.n_ctas, KM_THREADS, KmCfg<D>::SMEM, s, p);
   if (e != cudaSuccess) return e;
-  return launch_key_mass_add(a, QR, KM_KEYS, 2, s);
+  return launch_key_mass_add(a, KM_KEYS, 2, s);
 }
 }  // namespace
 

@@ -232,6 +232,7 @@ cudaError_t launch_gemm_tc(const TcGemmArgs &a, int num_sms, int *err, cudaStrea
 constexpr int KP_OV = 2;          // a unit's start-up and epilogue, in tile times
 constexpr int KP_MIN_CHUNK = 4;   // least share of a CTA, in tile times
 constexpr int KP_JOIN_NUM = 1, KP_JOIN_DEN = 16;   // joining one packed row, in tile times
+constexpr int KEY_PLAN_WORDS = 512;
 struct KeyArgs {
   int dtype, batch, n_ctx, M, H, Hkv, G, D;   // G = H / Hkv query heads per K/V head
   int prefix_len;
@@ -244,7 +245,8 @@ struct KeyArgs {
   float *lse;                     // attention: written (may be null); weight: read
   const float *mass_prev;
   float *mass, decay;
-  float *ws;                      // key_ws_floats(...)
+  float *ws;                      // key_attn_ws_floats / key_mass_ws_floats
+  int *plan;                      // KEY_PLAN_WORDS, the first kernel's plan for the second
   int n_ctas;                     // CTAs of the launch (attention / weight)
   int *err;
   unsigned long long wait_ns;
@@ -267,11 +269,10 @@ bool key_attn_tc_takes(int dtype, int D);
 cudaError_t launch_key_attn_tc(const KeyArgs &a, cudaStream_t s);
 cudaError_t key_mass_tc_setup(int D);
 cudaError_t launch_key_mass_tc(const KeyArgs &a, cudaStream_t s);
-// Adds the weights that a weight kernel left: units of kt keys, blocks of uq
-// query rows, `parts` sums a key.
-cudaError_t launch_key_mass_add(const KeyArgs &a, int uq, int kt, int parts, cudaStream_t s);
-// Joins partial rows: slots of rt packed rows, units of uq query rows, tiles of kt keys.
-cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, int kt, cudaStream_t s);
+// Adds the weights that a weight kernel left: units of kt keys, `parts` sums a key.
+cudaError_t launch_key_mass_add(const KeyArgs &a, int kt, int parts, cudaStream_t s);
+// Joins partial rows: slots of rt packed rows, units of uq query rows.
+cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, cudaStream_t s);
 
 // ------------------------------------------------------------------- evict.cu
 int evict_max_ctx();

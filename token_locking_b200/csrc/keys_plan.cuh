@@ -20,9 +20,9 @@ namespace sl {
 constexpr int KP_JOBS = SL_MAX_BATCH + 1;
 
 struct KeyPlan {
-  int q0[SL_MAX_BATCH + 1];   // first row of each sequence (clamped, ascending); [batch] = end
+  int q0[SL_MAX_BATCH + 1];   // first row of each sequence (clamped, ascending); from [batch] the end
   int kl[SL_MAX_BATCH];       // keys of each sequence's set, in [0, n_ctx]
-  int wbase[KP_JOBS + 1];     // first virtual tile of each job; [njobs] = W
+  int wbase[KP_JOBS + 1];     // first virtual tile of each job; from [njobs] W
   int T[KP_JOBS];             // inner tiles of a unit of the job
   int njobs, stacked, chunk, empty;   // empty: some sequence has rows and no keys
 };
@@ -45,92 +45,103 @@ __device__ __forceinline__ int warp_incl_sum(int v, int lane) {
   return v;
 }
 
-// Built by warp 0 (all 32 lanes); the caller synchronises the block after it.
+// Built by one warp (all 32 lanes); the caller synchronises the block after it.
 // weight = false: attention, units of uq rows, T = prefix and own key tiles of
 // kt keys, one unit per K/V head.  weight = true: units of kt keys, T = the
-// row blocks of uq rows of every K/V head.
+// row blocks of uq rows of every K/V head.  A lane holds sequences `lane` and
+// `32 + lane`: every operand is loaded at once and the rest is registers, since
+// all other warps of the launch wait for it.
 __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int kt, int n_ctas,
                                       bool weight, int lane) {
-  const int B = a.batch;
-  // row offsets, clamped into [0, M] and made ascending: a bad offset can only
-  // shorten a sequence, never send a row index out of range
-  int carry = 0;
-  for (int c = 0; c <= B; c += 32) {
-    const int i = c + lane;
-    int v = i <= B ? min(max(a.seq_off[i], 0), a.M) : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) v = max(v, __shfl_up_sync(0xffffffffu, v, o));
-    v = max(v, carry);
-    if (i <= B) pl.q0[i] = v;
-    carry = __shfl_sync(0xffffffffu, v, 31);
+  static_assert(SL_MAX_BATCH == 64, "two sequences per lane");
+  const int B = a.batch, b0 = lane, b1 = lane + 32;
+  int v0 = a.seq_off[min(b0, B)], v1 = a.seq_off[min(b1, B)], ve = a.seq_off[B];
+  int k0 = a.n_ctx, k1 = a.n_ctx;
+  if (a.key_len) {
+    k0 = a.key_len[min(b0, B - 1)];
+    k1 = a.key_len[min(b1, B - 1)];
   }
-  __syncwarp();
+  // row offsets, clamped into [0, M] and made ascending: a bad offset can only
+  // shorten a sequence, never send a row index out of range; sequences behind
+  // the last have no rows
+  v0 = min(max(v0, 0), a.M);
+  v1 = min(max(v1, 0), a.M);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    v0 = max(v0, __shfl_up_sync(0xffffffffu, v0, o));
+    v1 = max(v1, __shfl_up_sync(0xffffffffu, v1, o));
+  }
+  v1 = max(v1, __shfl_sync(0xffffffffu, v0, 31));
+  ve = max(min(max(ve, 0), a.M), __shfl_sync(0xffffffffu, v1, 31));
+  k0 = b0 < B ? min(max(k0, 0), a.n_ctx) : 0;
+  k1 = b1 < B ? min(max(k1, 0), a.n_ctx) : 0;
+  const int first = __shfl_sync(0xffffffffu, v0, 0);
+  int e0 = __shfl_down_sync(0xffffffffu, v0, 1), e1 = __shfl_down_sync(0xffffffffu, v1, 1);
+  const int v1_0 = __shfl_sync(0xffffffffu, v1, 0);
+  if (lane == 31) {
+    e0 = v1_0;
+    e1 = ve;
+  }
+  pl.q0[b0] = v0;
+  pl.q0[b1] = v1;
+  pl.kl[b0] = k0;
+  pl.kl[b1] = k1;
+  const int rows = ve - first;
   const int tp = weight ? 0 : kp_tiles(a.prefix_len, kt);
+  const int u0 = kp_tiles(e0 - v0, uq), u1 = kp_tiles(e1 - v1, uq);   // row blocks
+  const int t0 = kp_tiles(k0, kt), t1 = kp_tiles(k1, kt);             // own key tiles
   // tiles of both layouts: the prefix in every sequence's list, or once for
   // the rows of all sequences together
-  int cat = 0, own = 0, emp = 0;
-  for (int b = lane; b < B; b += 32) {
-    const int n = a.key_len ? min(max(a.key_len[b], 0), a.n_ctx) : a.n_ctx;
-    pl.kl[b] = n;
-    const int qn = pl.q0[b + 1] - pl.q0[b], nu = kp_tiles(qn, uq), to = kp_tiles(n, kt);
-    cat += tp + to > 0 ? nu * (tp + to + KP_OV) : 0;
-    own += to > 0 ? nu * (to + KP_OV) : 0;
-    emp |= qn > 0 && tp + to == 0;
-  }
-  __syncwarp();
-  cat = warp_sum_i(cat);
-  own = warp_sum_i(own);
-  emp = __any_sync(0xffffffffu, emp);
-  const int rows = pl.q0[B] - pl.q0[0];
   bool stacked = false;
+  const bool empty = __any_sync(0xffffffffu, (u0 > 0 && tp + t0 == 0) || (u1 > 0 && tp + t1 == 0));
+  const int nu_p = kp_tiles(rows, uq);
   if (a.stack && tp > 0) {
+    const int cat = warp_sum_i(u0 * (tp + t0 + KP_OV) + u1 * (tp + t1 + KP_OV));
+    const int own = warp_sum_i((t0 > 0 ? u0 * (t0 + KP_OV) : 0) + (t1 > 0 ? u1 * (t1 + KP_OV) : 0));
     // the joined layout reads the prefix once per block of rows of any
     // sequence, but each row's two partial results pass through memory
-    const int once = kp_tiles(rows, uq) * (tp + KP_OV) + own;
+    const int once = nu_p * (tp + KP_OV) + own;
     const int join = (int)((long long)rows * a.G * KP_JOIN_NUM / KP_JOIN_DEN);
     stacked = once + join < cat;
   }
-  // jobs and their first virtual tiles
-  const int njobs = B + (stacked ? 1 : 0);
-  int base = 0;
-  for (int c = 0; c < njobs; c += 32) {
-    const int j = c + lane;
-    int T = 0, cost = 0;
-    if (j < njobs) {
-      int nu;
-      if (stacked && j == 0) {
-        T = tp;
-        nu = kp_tiles(rows, uq);
-      } else {
-        const int b = stacked ? j - 1 : j;
-        const int qn = pl.q0[b + 1] - pl.q0[b];
-        if (weight) {
-          T = kp_tiles(qn, uq) * a.Hkv;
-          nu = kp_tiles(pl.kl[b], kt);
-        } else {
-          T = (stacked ? 0 : tp) + kp_tiles(pl.kl[b], kt);
-          nu = kp_tiles(qn, uq) * a.Hkv;
-        }
-      }
-      if (stacked && j == 0) nu *= a.Hkv;
-      cost = T > 0 ? nu * (T + KP_OV) : 0;
-    }
-    const int inc = warp_incl_sum(cost, lane);
-    if (j < njobs) {
-      pl.T[j] = T;
-      pl.wbase[j] = base + inc - cost;
-    }
-    base += __shfl_sync(0xffffffffu, inc, 31);
-  }
+  // jobs (the shared prefix first, where it is one) and their first virtual tiles
+  const int sh = stacked ? 1 : 0;
+  const int T0 = weight ? u0 * a.Hkv : (stacked ? 0 : tp) + t0;
+  const int T1 = weight ? u1 * a.Hkv : (stacked ? 0 : tp) + t1;
+  const int c0 = T0 > 0 ? (weight ? t0 : u0 * a.Hkv) * (T0 + KP_OV) : 0;
+  const int c1 = T1 > 0 ? (weight ? t1 : u1 * a.Hkv) * (T1 + KP_OV) : 0;
+  const int cp = stacked ? nu_p * a.Hkv * (tp + KP_OV) : 0;
+  const int i0 = warp_incl_sum(c0, lane), i1 = warp_incl_sum(c1, lane);
+  const int half = cp + __shfl_sync(0xffffffffu, i0, 31);
+  const int W = half + __shfl_sync(0xffffffffu, i1, 31);
+  pl.T[b0 + sh] = T0;
+  pl.T[b1 + sh] = T1;
+  pl.wbase[b0 + sh] = cp + i0 - c0;
+  pl.wbase[b1 + sh] = half + i1 - c1;
   if (lane == 0) {
-    pl.wbase[njobs] = base;
-    pl.njobs = njobs;
+    if (stacked) {
+      pl.T[0] = tp;
+      pl.wbase[0] = 0;
+    }
+    pl.q0[64] = ve;
+    pl.wbase[64 + sh] = W;
+    pl.njobs = B + sh;
     pl.stacked = stacked;
-    pl.empty = emp;
-    const int share = (base + n_ctas - 1) / n_ctas;
-    pl.chunk = max(share, KP_MIN_CHUNK);
+    pl.empty = empty;
+    pl.chunk = max((W + n_ctas - 1) / n_ctas, KP_MIN_CHUNK);
   }
   __syncwarp();
+}
+
+// The plan of a launch, for the kernel that follows it: written by one block
+// (`n` threads, the plan complete and synchronised), read by all of the next.
+constexpr int KP_WORDS = sizeof(KeyPlan) / 4;
+static_assert(KP_WORDS <= KEY_PLAN_WORDS, "the workspace holds the plan");
+__device__ __forceinline__ void key_plan_publish(const KeyPlan &pl, int *to, int tid, int n) {
+  for (int i = tid; i < KP_WORDS; i += n) to[i] = reinterpret_cast<const int *>(&pl)[i];
+}
+__device__ __forceinline__ void key_plan_fetch(KeyPlan &pl, const int *from, int tid, int n) {
+  for (int i = tid; i < KP_WORDS; i += n) reinterpret_cast<int *>(&pl)[i] = __ldcg(from + i);
 }
 
 // Sequence of job j, or -1 for the shared prefix's job.

@@ -439,30 +439,48 @@ class Sampler:
             pass
 
 
-def _rows_ptr(t: torch.Tensor, name: str, device, dtype, n_rows=None):
-    """(pointer, row stride) of a 2-D operand with unit column stride."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _rows_ptr(t: torch.Tensor, name: str, device: int, dtype, cols: int, n_rows=None):
+    """(pointer, row stride) of a [rows, cols] operand with unit column stride."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if n_rows is not None and t.shape[0] != n_rows:
-        raise ValueError(f"{name} has {t.shape[0]} rows, expected {n_rows}")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    (n, c), (ld, step) = t.shape, t.stride()
+    if c != cols:
+        raise ValueError(f"{name} has {c} columns, expected {cols}")
+    if n_rows is not None and n != n_rows:
+        raise ValueError(f"{name} has {n} rows, expected {n_rows}")
+    if step != 1 and c > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), (ld if n > 1 else c)
 
 
-def _dense_ptr(t: Optional[torch.Tensor], name: str, device, dtype, shape):
+def _dense_ptr(t: Optional[torch.Tensor], name: str, device: int, dtype, shape):
     """Pointer of a contiguous tensor of the given shape (None stays None)."""
     if t is None:
         return None
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}")
     return t.data_ptr()
+
+
+def _call_on(device: int, fn, name: str, stream, *args):
+    """A library call with the operands' device current, on the given stream or
+    that device's current one."""
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, raw)
+    if st != A.SL_OK:
+        A.check(st, name)
 
 
 class KeyAttention:
@@ -488,14 +506,10 @@ class KeyAttention:
         self.device = torch.device("cuda", torch.cuda.current_device())
 
     def _set(self, seq_off, key_len, keys):
-        B = self.batch
-        return A.KeySet(_dense_ptr(seq_off, "seq_off", self.device, torch.int32, (B + 1,)),
-                        _dense_ptr(key_len, "key_len", self.device, torch.int32, (B,)),
-                        _dense_ptr(keys, "keys", self.device, torch.int32, (B, self.n_ctx)))
-
-    def _width(self, t, name, heads):
-        if t.shape[1] != heads * self.head_dim:
-            raise ValueError(f"{name} has {t.shape[1]} columns, expected {heads * self.head_dim}")
+        B, dev, i32 = self.batch, self.device.index, torch.int32
+        return A.KeySet(_dense_ptr(seq_off, "seq_off", dev, i32, (B + 1,)),
+                        _dense_ptr(key_len, "key_len", dev, i32, (B,)),
+                        _dense_ptr(keys, "keys", dev, i32, (B, self.n_ctx)))
 
     def attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                seq_off: torch.Tensor, key_len: Optional[torch.Tensor] = None,
@@ -504,14 +518,13 @@ class KeyAttention:
                stream=None):
         """o [rows, n_heads * head_dim] (and lse [rows, n_heads] fp32) of q over
         k, v [batch * n_ctx, n_kv_heads * head_dim] and the prefix [P, same]."""
-        dev, dt, rows = self.device, self.torch_dtype, q.shape[0]
-        pq, lq = _rows_ptr(q, "q", dev, dt)
-        pk, lk = _rows_ptr(k, "k", dev, dt, self.batch * self.n_ctx)
-        pv, lv = _rows_ptr(v, "v", dev, dt, self.batch * self.n_ctx)
-        po, lo = _rows_ptr(o, "o", dev, dt, rows)
-        for t, name, heads in ((q, "q", self.n_heads), (k, "k", self.n_kv_heads),
-                               (v, "v", self.n_kv_heads), (o, "o", self.n_heads)):
-            self._width(t, name, heads)
+        dev, dt, rows = self.device.index, self.torch_dtype, q.shape[0]
+        hd, hkd, n = self.n_heads * self.head_dim, self.n_kv_heads * self.head_dim, \
+            self.batch * self.n_ctx
+        pq, lq = _rows_ptr(q, "q", dev, dt, hd)
+        pk, lk = _rows_ptr(k, "k", dev, dt, hkd, n)
+        pv, lv = _rows_ptr(v, "v", dev, dt, hkd, n)
+        po, lo = _rows_ptr(o, "o", dev, dt, hd, rows)
         if lk != lv:
             raise ValueError("k and v must have the same row stride")
         if (k_prefix is None) != (v_prefix is None):
@@ -520,18 +533,14 @@ class KeyAttention:
         lp = n_prefix = 0
         if k_prefix is not None and k_prefix.shape[0] > 0:
             n_prefix = k_prefix.shape[0]
-            pkp, lp = _rows_ptr(k_prefix, "k_prefix", dev, dt)
-            pvp, lvp = _rows_ptr(v_prefix, "v_prefix", dev, dt, n_prefix)
-            self._width(k_prefix, "k_prefix", self.n_kv_heads)
-            self._width(v_prefix, "v_prefix", self.n_kv_heads)
+            pkp, lp = _rows_ptr(k_prefix, "k_prefix", dev, dt, hkd)
+            pvp, lvp = _rows_ptr(v_prefix, "v_prefix", dev, dt, hkd, n_prefix)
             if lp != lvp:
                 raise ValueError("k_prefix and v_prefix must have the same row stride")
         ks = self._set(seq_off, key_len, keys)
         pl = _dense_ptr(lse, "lse", dev, torch.float32, (rows, self.n_heads))
-        with torch.cuda.device(dev):
-            A.check(A.lib().sl_key_attention(self.handle, rows, pq, lq, pk, pv, lk, C.byref(ks),
-                                             pkp, pvp, lp, n_prefix, po, lo, pl,
-                                             _stream(stream)), "sl_key_attention")
+        _call_on(dev, A.lib().sl_key_attention, "sl_key_attention", stream, self.handle, rows, pq,
+                 lq, pk, pv, lk, C.byref(ks), pkp, pvp, lp, n_prefix, po, lo, pl)
 
     def mass(self, q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, mass: torch.Tensor,
              seq_off: torch.Tensor, key_len: Optional[torch.Tensor] = None,
@@ -539,19 +548,16 @@ class KeyAttention:
              decay: float = 0.0, stream=None):
         """mass [batch, n_ctx] = decay * mass_prev + the attention weight each key
         of the sets receives from the rows of q, given their lse."""
-        dev, rows = self.device, q.shape[0]
-        pq, lq = _rows_ptr(q, "q", dev, self.torch_dtype)
-        pk, lk = _rows_ptr(k, "k", dev, self.torch_dtype, self.batch * self.n_ctx)
-        self._width(q, "q", self.n_heads)
-        self._width(k, "k", self.n_kv_heads)
+        dev, rows, shape = self.device.index, q.shape[0], (self.batch, self.n_ctx)
+        pq, lq = _rows_ptr(q, "q", dev, self.torch_dtype, self.n_heads * self.head_dim)
+        pk, lk = _rows_ptr(k, "k", dev, self.torch_dtype, self.n_kv_heads * self.head_dim,
+                           self.batch * self.n_ctx)
         ks = self._set(seq_off, key_len, keys)
-        shape = (self.batch, self.n_ctx)
         pl = _dense_ptr(lse, "lse", dev, torch.float32, (rows, self.n_heads))
         pp = _dense_ptr(mass_prev, "mass_prev", dev, torch.float32, shape)
         pm = _dense_ptr(mass, "mass", dev, torch.float32, shape)
-        with torch.cuda.device(dev):
-            A.check(A.lib().sl_key_mass(self.handle, rows, pq, lq, pk, lk, C.byref(ks), pl, decay,
-                                        pp, pm, _stream(stream)), "sl_key_mass")
+        _call_on(dev, A.lib().sl_key_mass, "sl_key_mass", stream, self.handle, rows, pq, lq, pk,
+                 lk, C.byref(ks), pl, decay, pp, pm)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -571,15 +577,14 @@ def kv_evict(mass: torch.Tensor, budget: int, keys: torch.Tensor, key_len: torch
     """Keep the protected entries and the heaviest others up to `budget` per
     sequence (sl_kv_evict): ascending kept positions into keys [batch, n_ctx],
     their number into key_len [batch], flags into present_out."""
-    dev = mass.device
     if not mass.is_cuda or mass.dim() != 2:
         raise ValueError("mass must be a CUDA tensor [batch, n_ctx]")
-    B, N = mass.shape
-    args = [_dense_ptr(mass, "mass", dev, torch.float32, (B, N)),
-            _dense_ptr(protect, "protect", dev, torch.uint8, (B, N)),
-            _dense_ptr(present, "present", dev, torch.uint8, (B, N)),
-            _dense_ptr(keys, "keys", dev, torch.int32, (B, N)),
-            _dense_ptr(key_len, "key_len", dev, torch.int32, (B,)),
-            _dense_ptr(present_out, "present_out", dev, torch.uint8, (B, N))]
-    with torch.cuda.device(dev):
-        A.check(A.lib().sl_kv_evict(B, N, int(budget), *args, _stream(stream)), "sl_kv_evict")
+    B, N = shape = tuple(mass.shape)
+    dev, u8 = mass.get_device(), torch.uint8
+    _call_on(dev, A.lib().sl_kv_evict, "sl_kv_evict", stream, B, N, int(budget),
+             _dense_ptr(mass, "mass", dev, torch.float32, shape),
+             _dense_ptr(protect, "protect", dev, u8, shape),
+             _dense_ptr(present, "present", dev, u8, shape),
+             _dense_ptr(keys, "keys", dev, torch.int32, shape),
+             _dense_ptr(key_len, "key_len", dev, torch.int32, (B,)),
+             _dense_ptr(present_out, "present_out", dev, u8, shape))
