@@ -52,9 +52,9 @@ sl_status fill_args(const sl_key_attn *a, const char *fn, int rows, const void *
                 c.n_kv_heads * c.head_dim);
   if (prefix_len < 0) return fail(SL_ERR_INVALID, "%s: prefix_len %d < 0", fn, prefix_len);
   // the work plan counts (row block, head, key tile) triples in 32 bits
-  const double tiles = (double)(prefix_len + (double)c.n_ctx) / 64.0 + 2 + KP_OV;
+  const double tiles = (double)(prefix_len + (double)c.n_ctx) / 64.0 + 4;
   const double blocks = c.n_kv_heads * ((double)rows * a->group / 32.0 + 2.0 * c.batch);
-  if (tiles * (blocks + (double)KP_OV * c.batch) > 1e9)
+  if (tiles * (blocks + 2.0 * c.batch) > 1e9)
     return fail(SL_ERR_UNSUPPORTED, "%s: rows x keys x heads too large for one call", fn);
   *x = KeyArgs{};
   x->dtype = c.dtype;

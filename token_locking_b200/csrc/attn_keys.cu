@@ -201,11 +201,13 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
 // ------------------------------------------------------------------- joining --
 // Partial rows (max m in base 2, sum l, unnormalised o) of one (row, head)
 // joined in the order of the CTAs that left them: o = sum_i 2^(m_i - m) o_i / L,
-// L = sum_i 2^(m_i - m) l_i.  One warp per (row, head), lanes over the columns.
-// Without a joint prefix only units that a CTA's share cut have partial rows:
-// blockIdx.x = c looks at the cut at the start of CTA c's share, and the first
-// cut of a unit joins it, blockIdx.y sharing its rows.  With one, every row
-// does (one part from the prefix, one from its sequence's own keys).
+// L = sum_i 2^(m_i - m) l_i.  Lanes over the columns; nw warps of a block share
+// one row's pieces where there are few rows, and their sums are joined in warp
+// order.  Without a joint prefix only units that a CTA's share cut have partial
+// rows: blockIdx.x = c looks at the cut at the start of CTA c's share, and the
+// first cut of a unit joins it, blockIdx.y sharing its rows.  With one, every
+// row does (one part from the prefix, one from its sequence's own keys).
+constexpr int KJ_WARPS = 8, KJ_Y = 8;         // warps of a block, blocks per cut
 struct JoinAcc {
   float m, l;
   float4 o;
@@ -234,29 +236,30 @@ __device__ __forceinline__ void join_store(const KeyArgs &a, const JoinAcc &x, i
     a.lse[(size_t)row * a.H + h] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * KEY_LN2;
 }
 
-// The pieces of one unit of job j (row offset inside it: packed row r).
+// Pieces sub, sub + nw, ... of one unit of job j (its packed row r).
 __device__ __forceinline__ void join_unit(const KeyArgs &a, const KeyPlan &pl, JoinAcc &x, int j,
                                           int unit, int hk, int r, int rt, int row, int h,
-                                          int lane) {
+                                          int lane, int sub, int nw) {
   const int T = pl.T[j];
   if (T == 0) return;
-  const int wu = pl.wbase[j] + (unit * a.Hkv + hk) * (T + KP_OV);
+  const int wu = pl.wbase[j] + (unit * a.Hkv + hk) * (T + pl.ov);
   const KeyRecs recs(a, rt);
-  const int c1 = (wu + T + KP_OV - 1) / pl.chunk;
+  const int c1 = (wu + T + pl.ov - 1) / pl.chunk;
   constexpr int U = 2;                                 // pieces whose loads are in flight together
-  for (int c = wu / pl.chunk; c <= c1; c += U) {
+  for (int c = wu / pl.chunk + sub; c <= c1; c += U * nw) {
     float2 ml[U];
     float4 u[U];
     bool on[U];
 #pragma unroll
     for (int e = 0; e < U; ++e) {
+      const int ce = c + e * nw;
       int t0 = 0, t1 = 0;
-      if (c + e <= c1) kp_piece_of(pl, wu, T, c + e, t0, t1);
+      if (ce <= c1) kp_piece_of(pl, wu, T, ce, t0, t1);
       on[e] = t1 > t0;
       if (on[e]) {
         const size_t rec = t0 == 0 && t1 == T
                                ? key_rec_row(a, rt, kp_seq(pl, j) < 0 ? 0 : 1, row, h)
-                               : key_rec_slot(kp_slot(c + e, t0), rt, r);
+                               : key_rec_slot(kp_slot(ce, t0), rt, r);
         ml[e] = __ldcg(recs.ml + rec);
         if (4 * lane < a.D)
           u[e] = __ldcg(reinterpret_cast<const float4 *>(recs.o + rec * a.D + 4 * lane));
@@ -268,29 +271,58 @@ __device__ __forceinline__ void join_unit(const KeyArgs &a, const KeyPlan &pl, J
   }
 }
 
+// Warps per row: as many as leave every row a place at once.
+__device__ __forceinline__ int join_warps(long long rows, long long warps) {
+  return rows * 8 <= warps ? 8 : rows * 4 <= warps ? 4 : rows * 2 <= warps ? 2 : 1;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(256, 4) key_join_kernel(const KeyArgs a, int rt, int uq) {
+__global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArgs a, int rt,
+                                                                     int uq) {
   __shared__ KeyPlan pl;
+  __shared__ JoinAcc part[KJ_WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  key_plan_fetch(pl, a.plan, threadIdx.x, 256);
+  key_plan_fetch(pl, a.plan, threadIdx.x, 32 * KJ_WARPS);
   __syncthreads();
+  const JoinAcc none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  // the block's warps that share a row join their sums and write it
+  auto finish = [&](JoinAcc &x, int nw, int sub, bool there, int row, int h) {
+    if (nw > 1) {
+      part[warp][lane] = x;
+      __syncthreads();
+      if (there && sub == 0)
+        for (int e = 1; e < nw; ++e) {
+          const JoinAcc &y = part[warp + e][lane];
+          join_rec(x, make_float2(y.m, y.l), y.o);
+        }
+    }
+    if (there && sub == 0) join_store<T>(a, x, row, h, lane);
+    if (nw > 1) __syncthreads();
+  };
   const int W = pl.wbase[pl.njobs];
-  const int n_warps = gridDim.x * gridDim.y * 8;
-  const int gw = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp;
+  const int blk = blockIdx.y * gridDim.x + blockIdx.x, n_blks = gridDim.x * gridDim.y;
   if (pl.stacked) {
-    const int rows = pl.q0[a.batch] - pl.q0[0];
+    const long long items = (long long)(pl.q0[a.batch] - pl.q0[0]) * a.H;
+    const int nw = join_warps(items, (long long)n_blks * KJ_WARPS);
+    const int sub = warp % nw, per = KJ_WARPS / nw;
     int b = 0;
-    for (long long i = gw; i < (long long)rows * a.H; i += n_warps) {
-      const int row = pl.q0[0] + (int)(i / a.H), h = (int)(i % a.H);
-      const int hk = h / a.G, g = h % a.G;
-      while (pl.q0[b + 1] <= row) ++b;
-      JoinAcc x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      const int rp = row - pl.q0[0], ro = row - pl.q0[b];
-      join_unit(a, pl, x, 0, rp / uq, hk, (rp % uq) * a.G + g, rt, row, h, lane);
-      join_unit(a, pl, x, b + 1, ro / uq, hk, (ro % uq) * a.G + g, rt, row, h, lane);
-      join_store<T>(a, x, row, h, lane);
+    for (long long i0 = (long long)blk * per; i0 < items; i0 += (long long)n_blks * per) {
+      const long long i = i0 + warp / nw;
+      const bool there = i < items;
+      JoinAcc x = none;
+      int row = 0, h = 0;
+      if (there) {
+        row = pl.q0[0] + (int)(i / a.H);
+        h = (int)(i % a.H);
+        const int hk = h / a.G, g = h % a.G;
+        while (pl.q0[b + 1] <= row) ++b;
+        const int rp = row - pl.q0[0], ro = row - pl.q0[b];
+        join_unit(a, pl, x, 0, rp / uq, hk, (rp % uq) * a.G + g, rt, row, h, lane, sub, nw);
+        join_unit(a, pl, x, b + 1, ro / uq, hk, (ro % uq) * a.G + g, rt, row, h, lane, sub, nw);
+      }
+      finish(x, nw, sub, there, row, h);
     }
     return;
   }
@@ -298,9 +330,8 @@ __global__ void __launch_bounds__(256, 4) key_join_kernel(const KeyArgs a, int r
     for (int b = 0; b < a.batch; ++b) {
       if (pl.T[b] > 0) continue;
       const long long n = (long long)(pl.q0[b + 1] - pl.q0[b]) * a.H;
-      for (long long i = gw; i < n; i += n_warps)
-        join_store<T>(a, JoinAcc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)},
-                      pl.q0[b] + (int)(i / a.H), (int)(i % a.H), lane);
+      for (long long i = (long long)blk * KJ_WARPS + warp; i < n; i += (long long)n_blks * KJ_WARPS)
+        join_store<T>(a, none, pl.q0[b] + (int)(i / a.H), (int)(i % a.H), lane);
     }
   }
   const int c = blockIdx.x;
@@ -308,11 +339,11 @@ __global__ void __launch_bounds__(256, 4) key_join_kernel(const KeyArgs a, int r
   if (c == 0 || cut >= W) return;
   int j = 0;
   while (cut >= pl.wbase[j + 1]) ++j;
-  const int cu = pl.T[j] + KP_OV, u = ((int)cut - pl.wbase[j]) / cu;
+  const int cu = pl.T[j] + pl.ov, u = ((int)cut - pl.wbase[j]) / cu;
   const int wu = pl.wbase[j] + u * cu;
   // the unit's first cut joins it; a cut at its start is none
   if (cut == wu || (long long)(c - 1) * pl.chunk > wu) return;
-  if (cut - wu <= KP_OV) {
+  if (cut - wu <= pl.ov) {
     // the share before holds no tile of it: whole if this share ends it
     int t0, t1;
     kp_piece_of(pl, wu, pl.T[j], c, t0, t1);
@@ -321,11 +352,14 @@ __global__ void __launch_bounds__(256, 4) key_join_kernel(const KeyArgs a, int r
   const int unit = u / a.Hkv, hk = u - unit * a.Hkv;
   const int r0 = pl.q0[j] + unit * uq;
   const int rn = min(uq, pl.q0[j + 1] - r0) * a.G;
-  for (int r = blockIdx.y * 8 + warp; r < rn; r += gridDim.y * 8) {
-    JoinAcc x{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const int nw = join_warps(rn, KJ_WARPS * gridDim.y), sub = warp % nw, per = KJ_WARPS / nw;
+  for (int i0 = blockIdx.y * per; i0 < rn; i0 += gridDim.y * per) {
+    const int r = i0 + warp / nw;
+    const bool there = r < rn;
+    JoinAcc x = none;
     const int row = r0 + r / a.G, h = hk * a.G + r % a.G;
-    join_unit(a, pl, x, j, unit, hk, r, rt, row, h, lane);
-    join_store<T>(a, x, row, h, lane);
+    if (there) join_unit(a, pl, x, j, unit, hk, r, rt, row, h, lane, sub, nw);
+    finish(x, nw, sub, there, row, h);
   }
 }
 
@@ -360,13 +394,16 @@ size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows) {
 }
 
 cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, cudaStream_t s) {
-  const dim3 grid(a.n_ctas, 8);
-  return a.dtype == SL_BF16 ? launch_k(key_join_kernel<bf16>, grid, 256, 0, s, a, rt, uq)
-                            : launch_k(key_join_kernel<float>, grid, 256, 0, s, a, rt, uq);
+  const dim3 grid(a.n_ctas, KJ_Y);
+  return a.dtype == SL_BF16
+             ? launch_k(key_join_kernel<bf16>, grid, 32 * KJ_WARPS, 0, s, a, rt, uq)
+             : launch_k(key_join_kernel<float>, grid, 32 * KJ_WARPS, 0, s, a, rt, uq);
 }
 
-cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s) {
+cudaError_t launch_key_attn(KeyArgs a, cudaStream_t s) {
   if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_attn_tc(a, s);
+  a.ov = 1;
+  a.min_chunk = 1;
   return a.dtype == SL_BF16 ? run_simt<bf16>(a, s) : run_simt<float>(a, s);
 }
 

@@ -560,7 +560,9 @@ cudaError_t key_attn_tc_setup(int D) {
 
 bool key_attn_tc_takes(int dtype, int D) { return dtype == SL_BF16 && (D == 64 || D == 128); }
 
-cudaError_t launch_key_attn_tc(const KeyArgs &a, cudaStream_t s) {
+cudaError_t launch_key_attn_tc(KeyArgs a, cudaStream_t s) {
+  a.ov = 2;
+  a.min_chunk = 3;
   return a.D == 128 ? run_tc<128>(a, s) : run_tc<64>(a, s);
 }
 

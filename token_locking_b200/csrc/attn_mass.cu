@@ -130,8 +130,12 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
 // set.  An entry that a list names twice counts twice, so the additions are
 // atomic; a position that is named once receives one addition, and its result
 // does not depend on any order.
+// A block takes 32 entries at a time, its warps a unit's pieces in turn; the
+// warps' sums are added in warp order.
 __global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int kt, int parts) {
   __shared__ KeyPlan pl;
+  __shared__ float sum[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
   key_plan_fetch(pl, a.plan, threadIdx.x, 256);
@@ -139,22 +143,31 @@ __global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int 
   const int b = blockIdx.y;
   const int T = pl.T[b];
   if (T == 0) return;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < pl.kl[b]; i += gridDim.x * 256) {
-    const int wu = pl.wbase[b] + i / kt * (T + KP_OV);
-    const int c1 = (wu + T + KP_OV - 1) / pl.chunk;
+  for (int i0 = blockIdx.x * 32; i0 < pl.kl[b]; i0 += gridDim.x * 32) {
+    const int i = i0 + lane;                  // 32 entries lie in one unit
+    const int wu = pl.wbase[b] + i0 / kt * (T + pl.ov);
+    const int c1 = (wu + T + pl.ov - 1) / pl.chunk;
     float v = 0.f;
-    for (int c = wu / pl.chunk; c <= c1; ++c) {
+    for (int c = wu / pl.chunk + warp; c <= c1; c += 8) {
       int t0, t1;
       kp_piece_of(pl, wu, T, c, t0, t1);
       if (t1 <= t0) continue;
-      for (int q = 0; q < parts; ++q)
-        v += t0 == 0 && t1 == T
-                 ? __ldcg(a.ws + 2 * (size_t)a.n_ctas * parts * kt +
-                          ((size_t)q * a.batch + b) * a.n_ctx + i)
-                 : __ldcg(a.ws + ((size_t)kp_slot(c, t0) * parts + q) * kt + i % kt);
+      const bool whole = t0 == 0 && t1 == T;
+      if (whole && i >= pl.kl[b]) continue;
+      const float *src = whole ? a.ws + 2 * (size_t)a.n_ctas * parts * kt + (size_t)b * a.n_ctx + i
+                               : a.ws + (size_t)kp_slot(c, t0) * parts * kt + i % kt;
+      const size_t step = whole ? (size_t)a.batch * a.n_ctx : kt;
+      for (int q = 0; q < parts; ++q) v += __ldcg(src + q * step);
     }
-    const int pos = key_pos(a, b, i);
-    if (pos >= 0) atomicAdd(a.mass + (size_t)b * a.n_ctx + pos, v);
+    sum[warp][lane] = v;
+    __syncthreads();
+    if (warp == 0 && i < pl.kl[b]) {
+#pragma unroll
+      for (int e = 1; e < 8; ++e) v += sum[e][lane];
+      const int pos = key_pos(a, b, i);
+      if (pos >= 0) atomicAdd(a.mass + (size_t)b * a.n_ctx + pos, v);
+    }
+    __syncthreads();
   }
 }
 
@@ -189,12 +202,14 @@ size_t key_mass_ws_floats(int dtype, int D, int batch, int n_ctx, int n_ctas) {
 }
 
 cudaError_t launch_key_mass_add(const KeyArgs &a, int kt, int parts, cudaStream_t s) {
-  const dim3 grid(std::min((a.n_ctx + 255) / 256, 256), a.batch);
+  const dim3 grid(std::min((a.n_ctx + 31) / 32, 1024), a.batch);
   return launch_k(key_mass_add_kernel, grid, 256, 0, s, a, kt, parts);
 }
 
-cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s) {
+cudaError_t launch_key_mass(KeyArgs a, cudaStream_t s) {
   if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_mass_tc(a, s);
+  a.ov = 1;
+  a.min_chunk = 1;
   return a.dtype == SL_BF16 ? run_mass_simt<bf16>(a, s) : run_mass_simt<float>(a, s);
 }
 

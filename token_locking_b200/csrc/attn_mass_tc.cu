@@ -407,7 +407,9 @@ cudaError_t key_mass_tc_setup(int D) {
                                          KmCfg<64>::SMEM);
 }
 
-cudaError_t launch_key_mass_tc(const KeyArgs &a, cudaStream_t s) {
+cudaError_t launch_key_mass_tc(KeyArgs a, cudaStream_t s) {
+  a.ov = 1;
+  a.min_chunk = 2;
   return a.D == 128 ? run_mass_tc<128>(a, s) : run_mass_tc<64>(a, s);
 }
 

@@ -229,8 +229,6 @@ cudaError_t launch_gemm_tc(const TcGemmArgs &a, int num_sms, int *err, cudaStrea
 // ------------------------------------------------- attn_keys.cu, attn_mass.cu
 // Attention over a key set per sequence, and the attention weight each key
 // receives (see keys_plan.cuh for how the work is shared out).
-constexpr int KP_OV = 2;          // a unit's start-up and epilogue, in tile times
-constexpr int KP_MIN_CHUNK = 4;   // least share of a CTA, in tile times
 constexpr int KP_JOIN_NUM = 1, KP_JOIN_DEN = 16;   // joining one packed row, in tile times
 constexpr int KEY_PLAN_WORDS = 512;
 struct KeyArgs {
@@ -246,6 +244,7 @@ struct KeyArgs {
   const float *mass_prev;
   float *mass, decay;
   float *ws;                      // key_attn_ws_floats / key_mass_ws_floats
+  int ov, min_chunk;              // a unit's start-up and epilogue, least share of a CTA: tile times
   int *plan;                      // KEY_PLAN_WORDS, the first kernel's plan for the second
   int n_ctas;                     // CTAs of the launch (attention / weight)
   int *err;
@@ -262,13 +261,13 @@ int key_mass_ctas(int dtype, int D, int num_sms);
 // rows whose prefix is a job of its own, two per row and head.
 size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows);
 size_t key_mass_ws_floats(int dtype, int D, int batch, int n_ctx, int n_ctas);
-cudaError_t launch_key_attn(const KeyArgs &a, cudaStream_t s);
-cudaError_t launch_key_mass(const KeyArgs &a, cudaStream_t s);
+cudaError_t launch_key_attn(KeyArgs a, cudaStream_t s);
+cudaError_t launch_key_mass(KeyArgs a, cudaStream_t s);
 // bf16 heads of 64 and 128 on the tensor cores (attn_keys_tc.cu)
 bool key_attn_tc_takes(int dtype, int D);
-cudaError_t launch_key_attn_tc(const KeyArgs &a, cudaStream_t s);
+cudaError_t launch_key_attn_tc(KeyArgs a, cudaStream_t s);
 cudaError_t key_mass_tc_setup(int D);
-cudaError_t launch_key_mass_tc(const KeyArgs &a, cudaStream_t s);
+cudaError_t launch_key_mass_tc(KeyArgs a, cudaStream_t s);
 // Adds the weights that a weight kernel left: units of kt keys, `parts` sums a key.
 cudaError_t launch_key_mass_add(const KeyArgs &a, int kt, int parts, cudaStream_t s);
 // Joins partial rows: slots of rt packed rows, units of uq query rows.

@@ -4,7 +4,7 @@
 //
 // A job is a run of query rows against one list of key tiles; it is cut into
 // units (a block of rows, or of keys for the weight kernel) of T inner tiles
-// each.  All units laid end to end, each as OV + T virtual tiles (OV: its
+// each.  All units laid end to end, each as ov + T virtual tiles (ov: its
 // start-up and epilogue in tile times), make W virtual tiles, and CTA c of nC
 // takes [c chunk, (c + 1) chunk) of them: equal shares whatever the lengths,
 // with a unit cut where a share ends.  A cut unit leaves partial results in
@@ -24,7 +24,7 @@ struct KeyPlan {
   int kl[SL_MAX_BATCH];       // keys of each sequence's set, in [0, n_ctx]
   int wbase[KP_JOBS + 1];     // first virtual tile of each job; from [njobs] W
   int T[KP_JOBS];             // inner tiles of a unit of the job
-  int njobs, stacked, chunk, empty;   // empty: some sequence has rows and no keys
+  int njobs, stacked, chunk, ov, empty;   // empty: some sequence has rows and no keys
 };
 
 // One piece of a unit, as one CTA computes it.
@@ -54,6 +54,7 @@ __device__ __forceinline__ int warp_incl_sum(int v, int lane) {
 __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int kt, int n_ctas,
                                       bool weight, int lane) {
   static_assert(SL_MAX_BATCH == 64, "two sequences per lane");
+  const int ov = a.ov;
   const int B = a.batch, b0 = lane, b1 = lane + 32;
   int v0 = a.seq_off[min(b0, B)], v1 = a.seq_off[min(b1, B)], ve = a.seq_off[B];
   int k0 = a.n_ctx, k1 = a.n_ctx;
@@ -96,11 +97,11 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
   const bool empty = __any_sync(0xffffffffu, (u0 > 0 && tp + t0 == 0) || (u1 > 0 && tp + t1 == 0));
   const int nu_p = kp_tiles(rows, uq);
   if (a.stack && tp > 0) {
-    const int cat = warp_sum_i(u0 * (tp + t0 + KP_OV) + u1 * (tp + t1 + KP_OV));
-    const int own = warp_sum_i((t0 > 0 ? u0 * (t0 + KP_OV) : 0) + (t1 > 0 ? u1 * (t1 + KP_OV) : 0));
+    const int cat = warp_sum_i(u0 * (tp + t0 + ov) + u1 * (tp + t1 + ov));
+    const int own = warp_sum_i((t0 > 0 ? u0 * (t0 + ov) : 0) + (t1 > 0 ? u1 * (t1 + ov) : 0));
     // the joined layout reads the prefix once per block of rows of any
     // sequence, but each row's two partial results pass through memory
-    const int once = nu_p * (tp + KP_OV) + own;
+    const int once = nu_p * (tp + ov) + own;
     const int join = (int)((long long)rows * a.G * KP_JOIN_NUM / KP_JOIN_DEN);
     stacked = once + join < cat;
   }
@@ -108,9 +109,9 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
   const int sh = stacked ? 1 : 0;
   const int T0 = weight ? u0 * a.Hkv : (stacked ? 0 : tp) + t0;
   const int T1 = weight ? u1 * a.Hkv : (stacked ? 0 : tp) + t1;
-  const int c0 = T0 > 0 ? (weight ? t0 : u0 * a.Hkv) * (T0 + KP_OV) : 0;
-  const int c1 = T1 > 0 ? (weight ? t1 : u1 * a.Hkv) * (T1 + KP_OV) : 0;
-  const int cp = stacked ? nu_p * a.Hkv * (tp + KP_OV) : 0;
+  const int c0 = T0 > 0 ? (weight ? t0 : u0 * a.Hkv) * (T0 + ov) : 0;
+  const int c1 = T1 > 0 ? (weight ? t1 : u1 * a.Hkv) * (T1 + ov) : 0;
+  const int cp = stacked ? nu_p * a.Hkv * (tp + ov) : 0;
   const int i0 = warp_incl_sum(c0, lane), i1 = warp_incl_sum(c1, lane);
   const int half = cp + __shfl_sync(0xffffffffu, i0, 31);
   const int W = half + __shfl_sync(0xffffffffu, i1, 31);
@@ -127,8 +128,9 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
     pl.wbase[64 + sh] = W;
     pl.njobs = B + sh;
     pl.stacked = stacked;
+    pl.ov = ov;
     pl.empty = empty;
-    pl.chunk = max((W + n_ctas - 1) / n_ctas, KP_MIN_CHUNK);
+    pl.chunk = max((W + n_ctas - 1) / n_ctas, a.min_chunk);
   }
   __syncwarp();
 }
@@ -155,7 +157,7 @@ __device__ __forceinline__ bool key_next(const KeyPlan &pl, int heads, int &w, i
   w_end = min(w_end, pl.wbase[pl.njobs]);
   while (w < w_end) {
     while (w >= pl.wbase[job + 1]) ++job;
-    const int T = pl.T[job], cu = T + KP_OV;
+    const int T = pl.T[job], cu = T + pl.ov;
     const int rel = w - pl.wbase[job];
     const int u = rel / cu, v0 = rel - u * cu;
     const int v1 = min(cu, v0 + (w_end - w));
@@ -163,8 +165,8 @@ __device__ __forceinline__ bool key_next(const KeyPlan &pl, int heads, int &w, i
     p.unit = u / heads;
     p.hk = u - p.unit * heads;
     p.T = T;
-    p.t0 = max(0, v0 - KP_OV);
-    p.t1 = v1 - KP_OV;
+    p.t0 = max(0, v0 - pl.ov);
+    p.t1 = v1 - pl.ov;
     p.w_unit = w - v0;
     w += v1 - v0;
     if (p.t1 > p.t0) return true;
@@ -179,9 +181,9 @@ __device__ __forceinline__ int kp_slot(int cta, int t0) { return 2 * cta + (t0 >
 __device__ __forceinline__ void kp_piece_of(const KeyPlan &pl, int w_unit, int T, int c, int &t0,
                                             int &t1) {
   const int v0 = max(c * pl.chunk, w_unit) - w_unit;
-  const int v1 = min((long long)(c + 1) * pl.chunk, (long long)w_unit + T + KP_OV) - w_unit;
-  t0 = max(0, v0 - KP_OV);
-  t1 = v1 - KP_OV;
+  const int v1 = min((long long)(c + 1) * pl.chunk, (long long)w_unit + T + pl.ov) - w_unit;
+  t0 = max(0, v0 - pl.ov);
+  t1 = v1 - pl.ov;
 }
 
 }  // namespace sl
