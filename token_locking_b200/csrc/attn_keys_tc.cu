@@ -215,19 +215,19 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         }
         if (!key_wait(bar(C::B_E + st), ph ^ 1u, abort_flag, lim)) { ok = false; break; }
         if (by_row) {
-          const long long base = (long long)b * a.n_ctx * a.ld_kv + pc.hk * D + ch * 8;
+          // one position serves K and V: src_k + d_kv is V's row
+          const bf16 *src_k = (const bf16 *)a.k + (long long)b * a.n_ctx * a.ld_kv + pc.hk * D + ch * 8;
+          const ptrdiff_t d_kv = (const bf16 *)a.v - (const bf16 *)a.k;
+          const uint32_t d0 = dst + off;
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const bf16 *src = (const bf16 *)(kv ? a.v : a.k) + base;
-            const uint32_t d0 = dst + kv * C::SLOT + off;
-#pragma unroll
-            for (int i = 0; i < C::NI; ++i) {
-              const int ps = i * C::RPI < 32
-                                 ? __shfl_sync(0xffffffffu, pos, (i * C::RPI + g0) & 31)
-                                 : __shfl_sync(0xffffffffu, pos2, (i * C::RPI + g0) & 31);
-              key_copy16(d0 + i * 2 * C::RPI * 128 + ((i * 2 * C::RPI) & 4 ? sw1 : sw0),
-                        src + (ps < 0 ? 0 : ps) * a.ld_kv, ps >= 0);
-            }
+          for (int i = 0; i < C::NI; ++i) {
+            const int ps = i * C::RPI < 32
+                               ? __shfl_sync(0xffffffffu, pos, (i * C::RPI + g0) & 31)
+                               : __shfl_sync(0xffffffffu, pos2, (i * C::RPI + g0) & 31);
+            const bf16 *src = src_k + max(ps, 0) * a.ld_kv;
+            const uint32_t to = d0 + i * 2 * C::RPI * 128 + ((i * 2 * C::RPI) & 4 ? sw1 : sw0);
+            key_copy16(to, src, ps >= 0);
+            key_copy16(to + C::SLOT, src + d_kv, ps >= 0);
           }
           key_copy_commit();
           if (++pend == C::LAG) {
