@@ -50,8 +50,9 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
   const int d4 = D >> 2;
   const float c2 = a.scale * KEY_LOG2E;
 
-  int w = min((long long)blockIdx.x * pl.chunk, (long long)pl.wbase[pl.njobs]), job = 0;
-  const int w_end = min((long long)w + pl.chunk, (long long)pl.wbase[pl.njobs]);
+  int w = kp_bound(pl, blockIdx.x, lane);
+  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
+  int job = kp_job_at(pl, pl.wbase, w, lane);
   KeyPiece pc;
   while (key_next(pl, a.Hkv, w, w_end, job, pc)) {
     const int b = kp_seq(pl, pc.job);
@@ -201,13 +202,16 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
 // ------------------------------------------------------------------- joining --
 // Partial rows (max m in base 2, sum l, unnormalised o) of one (row, head)
 // joined in the order of the CTAs that left them: o = sum_i 2^(m_i - m) o_i / L,
-// L = sum_i 2^(m_i - m) l_i.  Lanes over the columns; nw warps of a block share
-// one row's pieces where there are few rows, and their sums are joined in warp
-// order.  Without a joint prefix only units that a CTA's share cut have partial
-// rows: blockIdx.x = c looks at the cut at the start of CTA c's share, and the
-// first cut of a unit joins it, blockIdx.y sharing its rows.  With one, every
-// row does (one part from the prefix, one from its sequence's own keys).
-constexpr int KJ_WARPS = 8, KJ_Y = 8;         // warps of a block, blocks per cut
+// L = sum_i 2^(m_i - m) l_i.  Lanes over the columns.  Bound by the latency of
+// the loads, so several are in flight per warp: of four rows at a time, or of
+// four pieces; where there are few rows, nw warps of a block share one row's
+// pieces and their sums are joined in warp order.  Without a joint prefix only
+// units that a CTA's share cut have partial rows: blockIdx.x = c looks at the
+// cut at the start of CTA c's share, and the first cut of a unit joins it,
+// blockIdx.y sharing its rows.  With one, every row does (one part from the
+// prefix, one from its sequence's own keys).  All blocks fit the GPU at once
+// (twice as many took 16 us of 48 at 300 rows and 32 heads a sequence).
+constexpr int KJ_WARPS = 8, KJ_Y = 4;         // warps of a block, blocks per cut
 struct JoinAcc {
   float m, l;
   float4 o;
@@ -236,40 +240,26 @@ __device__ __forceinline__ void join_store(const KeyArgs &a, const JoinAcc &x, i
     a.lse[(size_t)row * a.H + h] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * KEY_LN2;
 }
 
-// Pieces sub, sub + nw, ... of one unit of job j (its packed row r).
-__device__ __forceinline__ void join_unit(const KeyArgs &a, const KeyPlan &pl, JoinAcc &x, int j,
-                                          int unit, int hk, int r, int rt, int row, int h,
-                                          int lane, int sub, int nw) {
-  const int T = pl.T[j];
-  if (T == 0) return;
-  const int wu = pl.wbase[j] + (unit * a.Hkv + hk) * (T + pl.ov);
-  const KeyRecs recs(a, rt);
-  const int c1 = (wu + T + pl.ov - 1) / pl.chunk;
-  constexpr int U = 2;                                 // pieces whose loads are in flight together
-  for (int c = wu / pl.chunk + sub; c <= c1; c += U * nw) {
-    float2 ml[U];
-    float4 u[U];
-    bool on[U];
-#pragma unroll
-    for (int e = 0; e < U; ++e) {
-      const int ce = c + e * nw;
-      int t0 = 0, t1 = 0;
-      if (ce <= c1) kp_piece_of(pl, wu, T, ce, t0, t1);
-      on[e] = t1 > t0;
-      if (on[e]) {
-        const size_t rec = t0 == 0 && t1 == T
-                               ? key_rec_row(a, rt, kp_seq(pl, j) < 0 ? 0 : 1, row, h)
-                               : key_rec_slot(kp_slot(ce, t0), rt, r);
-        ml[e] = __ldcg(recs.ml + rec);
-        if (4 * lane < a.D)
-          u[e] = __ldcg(reinterpret_cast<const float4 *>(recs.o + rec * a.D + 4 * lane));
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < U; ++e)
-      if (on[e]) join_rec(x, ml[e], u[e]);
+// A unit of job j, the CTAs c0 .. c0 + n - 1 whose shares meet it.
+struct JoinUnit {
+  int j, wu, c0, n;
+  __device__ __forceinline__ JoinUnit(const KeyPlan &pl, FastDiv chunk, int job, int w_unit) {
+    j = job;
+    wu = w_unit;
+    c0 = kp_first(pl, chunk, wu);
+    n = pl.T[j] > 0 ? kp_last(pl, chunk, wu, pl.T[j]) - c0 + 1 : 0;
   }
-}
+  // Record of packed row r in the e-th of them, or -1 if it holds none of its
+  // tiles; row_rec: where a piece that is the whole unit left the row.
+  __device__ __forceinline__ long long rec(const KeyPlan &pl, int e, int rt, int r,
+                                           size_t row_rec) const {
+    int t0, t1;
+    kp_piece_of(pl, wu, pl.T[j], c0 + e, t0, t1);
+    if (t1 <= t0) return -1;
+    return t0 == 0 && t1 == pl.T[j] ? (long long)row_rec
+                                    : (long long)key_rec_slot(kp_slot(c0 + e, t0), rt, r);
+  }
+};
 
 // Warps per row: as many as leave every row a place at once.
 __device__ __forceinline__ int join_warps(long long rows, long long warps) {
@@ -277,16 +267,26 @@ __device__ __forceinline__ int join_warps(long long rows, long long warps) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArgs a, int rt,
-                                                                     int uq) {
+__global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArgs a, int rt, int uq,
+                                                                     FastDiv by_h, FastDiv by_g,
+                                                                     FastDiv by_uq) {
   __shared__ KeyPlan pl;
   __shared__ JoinAcc part[KJ_WARPS][32];
+  __shared__ FastDiv by_chunk;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
   key_plan_fetch(pl, a.plan, threadIdx.x, 32 * KJ_WARPS);
+  if (threadIdx.x == 0)
+    by_chunk = FastDiv::of(__ldcg(reinterpret_cast<const int *>(
+        &reinterpret_cast<const KeyPlan *>(a.plan)->chunk)));
   __syncthreads();
+  const FastDiv chunk = by_chunk;
+  const KeyRecs recs(a, rt);
   const JoinAcc none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  const float4 *ro = reinterpret_cast<const float4 *>(recs.o + 4 * lane);
+  const bool col = 4 * lane < a.D;
+  const int d4 = a.D >> 2;
   // the block's warps that share a row join their sums and write it
   auto finish = [&](JoinAcc &x, int nw, int sub, bool there, int row, int h) {
     if (nw > 1) {
@@ -301,26 +301,106 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
     if (there && sub == 0) join_store<T>(a, x, row, h, lane);
     if (nw > 1) __syncthreads();
   };
+  // pieces sub, sub + nw, ... of n, four in flight; rec(e) gives a record or -1
+  auto gather = [&](JoinAcc &x, int n, int sub, int nw, auto rec) {
+    for (int e = sub; e < n; e += 4 * nw) {
+      float2 ml[4];
+      float4 u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const long long i = e + k * nw < n ? rec(e + k * nw) : -1;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        u[k] = none.o;
+        if (i >= 0) {
+          ml[k] = __ldcg(recs.ml + i);
+          if (col) u[k] = __ldcg(ro + i * d4);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) join_rec(x, ml[k], u[k]);
+    }
+  };
+  // the pieces of four rows whose packed rows are `step` apart in one unit, n of
+  // them there; row, h: the first's, where the unit may be whole (part 0 or 1)
+  auto gather4 = [&](JoinAcc (&x)[4], const JoinUnit &un, int r, int step, int n, int part, int row,
+                     int h) {
+    for (int e = 0; e < un.n; ++e) {
+      int t0, t1;
+      kp_piece_of(pl, un.wu, pl.T[un.j], un.c0 + e, t0, t1);
+      if (t1 <= t0) continue;
+      const bool whole = t0 == 0 && t1 == pl.T[un.j];
+      const size_t i = whole ? key_rec_row(a, rt, part, row, h)
+                             : key_rec_slot(kp_slot(un.c0 + e, t0), rt, r);
+      const size_t st = whole ? a.H : step;
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        v[k] = none.o;
+        if (k < n) {
+          ml[k] = __ldcg(recs.ml + i + k * st);
+          if (col) v[k] = __ldcg(ro + (i + k * st) * d4);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) join_rec(x[k], ml[k], v[k]);
+    }
+  };
   const int W = pl.wbase[pl.njobs];
   const int blk = blockIdx.y * gridDim.x + blockIdx.x, n_blks = gridDim.x * gridDim.y;
   if (pl.stacked) {
-    const long long items = (long long)(pl.q0[a.batch] - pl.q0[0]) * a.H;
+    const int items = (pl.q0[a.batch] - pl.q0[0]) * a.H;   // below 2^31: the joint rows are few
     const int nw = join_warps(items, (long long)n_blks * KJ_WARPS);
+    if (nw == 1) {
+      // four rows of a head at a time, in runs that share both units: finding a
+      // row's units and pieces cost more than its loads
+      const int rows = pl.q0[a.batch] - pl.q0[0], groups = (rows + 3) / 4 * a.H;
+      int b = 0;
+      for (int i = blk * KJ_WARPS + warp; i < groups; i += n_blks * KJ_WARPS) {
+        const int grp = by_h.div(i), h = i - grp * a.H;
+        const int hk = by_g.div(h), g = h - hk * a.G;
+        const int end = min(4 * grp + 4, rows);
+        for (int rp = 4 * grp; rp < end;) {
+          const int row = pl.q0[0] + rp;
+          while (pl.q0[b + 1] <= row) ++b;
+          const int rb = row - pl.q0[b], up = by_uq.div(rp), ub = by_uq.div(rb);
+          const JoinUnit p(pl, chunk, 0, pl.wbase[0] + (up * a.Hkv + hk) * (pl.T[0] + pl.ov));
+          const JoinUnit o(pl, chunk, b + 1,
+                           pl.wbase[b + 1] + (ub * a.Hkv + hk) * (pl.T[b + 1] + pl.ov));
+          const int n = min(min(end, (up + 1) * uq) - rp, min(pl.q0[b + 1], pl.q0[b] + (ub + 1) * uq) - row);
+          JoinAcc x[4] = {none, none, none, none};
+          gather4(x, p, (rp - up * uq) * a.G + g, a.G, n, 0, row, h);
+          gather4(x, o, (rb - ub * uq) * a.G + g, a.G, n, 1, row, h);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < n) join_store<T>(a, x[k], row + k, h, lane);
+          rp += n;
+        }
+      }
+      return;
+    }
     const int sub = warp % nw, per = KJ_WARPS / nw;
     int b = 0;
-    for (long long i0 = (long long)blk * per; i0 < items; i0 += (long long)n_blks * per) {
-      const long long i = i0 + warp / nw;
+    for (int i0 = blk * per; i0 < items; i0 += n_blks * per) {
+      const int i = i0 + warp / nw;
       const bool there = i < items;
       JoinAcc x = none;
       int row = 0, h = 0;
       if (there) {
-        row = pl.q0[0] + (int)(i / a.H);
-        h = (int)(i % a.H);
-        const int hk = h / a.G, g = h % a.G;
+        const int rp = by_h.div(i);
+        h = i - rp * a.H;
+        row = pl.q0[0] + rp;
+        const int hk = by_g.div(h), g = h - hk * a.G;
         while (pl.q0[b + 1] <= row) ++b;
-        const int rp = row - pl.q0[0], ro = row - pl.q0[b];
-        join_unit(a, pl, x, 0, rp / uq, hk, (rp % uq) * a.G + g, rt, row, h, lane, sub, nw);
-        join_unit(a, pl, x, b + 1, ro / uq, hk, (ro % uq) * a.G + g, rt, row, h, lane, sub, nw);
+        const int rb = row - pl.q0[b], up = by_uq.div(rp), ub = by_uq.div(rb);
+        const JoinUnit p(pl, chunk, 0, pl.wbase[0] + (up * a.Hkv + hk) * (pl.T[0] + pl.ov));
+        const JoinUnit o(pl, chunk, b + 1, pl.wbase[b + 1] + (ub * a.Hkv + hk) * (pl.T[b + 1] + pl.ov));
+        const int r_p = (rp - up * uq) * a.G + g, r_o = (rb - ub * uq) * a.G + g;
+        gather(x, p.n + o.n, sub, nw, [&](int e) {
+          return e < p.n ? p.rec(pl, e, rt, r_p, key_rec_row(a, rt, 0, row, h))
+                         : o.rec(pl, e - p.n, rt, r_o, key_rec_row(a, rt, 1, row, h));
+        });
       }
       finish(x, nw, sub, there, row, h);
     }
@@ -336,30 +416,45 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
   }
   const int c = blockIdx.x;
   const long long cut = (long long)c * pl.chunk;
-  if (c == 0 || cut >= W) return;
-  int j = 0;
-  while (cut >= pl.wbase[j + 1]) ++j;
+  if (c == 0 || cut >= W || pl.per) return;
+  const int j = kp_job_at(pl, pl.wbase, (int)cut, lane);
   const int cu = pl.T[j] + pl.ov, u = ((int)cut - pl.wbase[j]) / cu;
   const int wu = pl.wbase[j] + u * cu;
-  // the unit's first cut joins it; a cut at its start is none
-  if (cut == wu || (long long)(c - 1) * pl.chunk > wu) return;
-  if (cut - wu <= pl.ov) {
-    // the share before holds no tile of it: whole if this share ends it
-    int t0, t1;
-    kp_piece_of(pl, wu, pl.T[j], c, t0, t1);
-    if (t1 == pl.T[j]) return;
+  if (cut == wu) return;                      // between two units
+  // its cuts share the rows: this is the k-th of n_cuts; none of them where all
+  // its tiles lie in one share, which then wrote the rows
+  const JoinUnit un(pl, chunk, j, wu);
+  const int n_cuts = un.n - 1, k = c - un.c0 - 1;
+  for (int e = 0, t0 = 0, t1 = 0; e < un.n && t1 == 0; ++e) {
+    kp_piece_of(pl, wu, pl.T[j], un.c0 + e, t0, t1);
+    if (t0 == 0 && t1 == pl.T[j]) return;
+    t1 = max(t1, 0);
   }
   const int unit = u / a.Hkv, hk = u - unit * a.Hkv;
   const int r0 = pl.q0[j] + unit * uq;
   const int rn = min(uq, pl.q0[j + 1] - r0) * a.G;
-  const int nw = join_warps(rn, KJ_WARPS * gridDim.y), sub = warp % nw, per = KJ_WARPS / nw;
-  for (int i0 = blockIdx.y * per; i0 < rn; i0 += gridDim.y * per) {
-    const int r = i0 + warp / nw;
-    const bool there = r < rn;
-    JoinAcc x = none;
-    const int row = r0 + r / a.G, h = hk * a.G + r % a.G;
-    if (there) join_unit(a, pl, x, j, unit, hk, r, rt, row, h, lane, sub, nw);
-    finish(x, nw, sub, there, row, h);
+  const int y = k * gridDim.y + blockIdx.y, n_y = n_cuts * gridDim.y;   // this block of the unit's
+  const int nw = join_warps(rn, (long long)KJ_WARPS * n_y), sub = warp % nw, per = KJ_WARPS / nw;
+  if (nw > 1) {
+    for (int i0 = y * per; i0 < rn; i0 += n_y * per) {
+      const int r = i0 + warp / nw;
+      const bool there = r < rn;
+      JoinAcc x = none;
+      const int rq = by_g.div(r);
+      if (there) gather(x, un.n, sub, nw, [&](int e) { return un.rec(pl, e, rt, r, 0); });
+      finish(x, nw, sub, there, r0 + rq, hk * a.G + r - rq * a.G);
+    }
+    return;
+  }
+  const int step = n_y * KJ_WARPS;
+  for (int ra = y * KJ_WARPS + warp; ra < rn; ra += 4 * step) {
+    JoinAcc x[4] = {none, none, none, none};
+    gather4(x, un, ra, step, (rn - ra + step - 1) / step, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = ra + k * step, rq = by_g.div(r);
+      if (r < rn) join_store<T>(a, x[k], r0 + rq, hk * a.G + r - rq * a.G, lane);
+    }
   }
 }
 
@@ -395,15 +490,18 @@ size_t key_attn_ws_floats(int dtype, int D, int H, int n_ctas, int stack_rows) {
 
 cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, cudaStream_t s) {
   const dim3 grid(a.n_ctas, KJ_Y);
+  const FastDiv by_h = FastDiv::of(a.H), by_g = FastDiv::of(a.G), by_uq = FastDiv::of(uq);
   return a.dtype == SL_BF16
-             ? launch_k(key_join_kernel<bf16>, grid, 32 * KJ_WARPS, 0, s, a, rt, uq)
-             : launch_k(key_join_kernel<float>, grid, 32 * KJ_WARPS, 0, s, a, rt, uq);
+             ? launch_k(key_join_kernel<bf16>, grid, 32 * KJ_WARPS, 0, s, a, rt, uq, by_h, by_g, by_uq)
+             : launch_k(key_join_kernel<float>, grid, 32 * KJ_WARPS, 0, s, a, rt, uq, by_h, by_g,
+                        by_uq);
 }
 
 cudaError_t launch_key_attn(KeyArgs a, cudaStream_t s) {
   if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_attn_tc(a, s);
   a.ov = 1;
   a.min_chunk = 1;
+  a.join_cost = 0;
   return a.dtype == SL_BF16 ? run_simt<bf16>(a, s) : run_simt<float>(a, s);
 }
 

@@ -144,9 +144,9 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   const int tp = kp_tiles(a.prefix_len, BN);
 
   // every role walks the same pieces
-  const int W = pl.wbase[pl.njobs];
-  int w = (int)min((long long)blockIdx.x * pl.chunk, (long long)W), job = 0;
-  const int w_end = (int)min((long long)w + pl.chunk, (long long)W);
+  int w = kp_bound(pl, blockIdx.x, lane);
+  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
+  int job = kp_job_at(pl, pl.wbase, w, lane);
   KeyPiece pc{};
   // first query row and query rows of a piece's unit; row tiles it fills
   auto rows_of = [&](int &r0, int &rn) {
@@ -563,6 +563,7 @@ bool key_attn_tc_takes(int dtype, int D) { return dtype == SL_BF16 && (D == 64 |
 cudaError_t launch_key_attn_tc(KeyArgs a, cudaStream_t s) {
   a.ov = 2;
   a.min_chunk = 3;
+  a.join_cost = 7;
   return a.D == 128 ? run_tc<128>(a, s) : run_tc<64>(a, s);
 }
 

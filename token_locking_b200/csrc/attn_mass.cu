@@ -41,8 +41,9 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   if (blockIdx.x == 0) key_plan_publish(pl, a.plan, tid, MS_THREADS);
   pdl_trigger();
   const float c2 = a.scale * KEY_LOG2E;
-  int w = min((long long)blockIdx.x * pl.chunk, (long long)pl.wbase[pl.njobs]), job = 0;
-  const int w_end = min((long long)w + pl.chunk, (long long)pl.wbase[pl.njobs]);
+  int w = kp_bound(pl, blockIdx.x, lane);
+  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
+  int job = kp_job_at(pl, pl.wbase, w, lane);
   KeyPiece pc;
   while (key_next(pl, 1, w, w_end, job, pc)) {
     const int b = pc.job;
@@ -146,9 +147,9 @@ __global__ void __launch_bounds__(256) key_mass_add_kernel(const KeyArgs a, int 
   for (int i0 = blockIdx.x * 32; i0 < pl.kl[b]; i0 += gridDim.x * 32) {
     const int i = i0 + lane;                  // 32 entries lie in one unit
     const int wu = pl.wbase[b] + i0 / kt * (T + pl.ov);
-    const int c1 = (wu + T + pl.ov - 1) / pl.chunk;
+    const int c0 = pl.per ? 0 : wu / pl.chunk, c1 = pl.per ? 0 : (wu + T + pl.ov - 1) / pl.chunk;
     float v = 0.f;
-    for (int c = wu / pl.chunk + warp; c <= c1; c += 8) {
+    for (int c = c0 + warp; c <= c1; c += 8) {
       int t0, t1;
       kp_piece_of(pl, wu, T, c, t0, t1);
       if (t1 <= t0) continue;
@@ -210,6 +211,7 @@ cudaError_t launch_key_mass(KeyArgs a, cudaStream_t s) {
   if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_mass_tc(a, s);
   a.ov = 1;
   a.min_chunk = 1;
+  a.join_cost = 0;
   return a.dtype == SL_BF16 ? run_mass_simt<bf16>(a, s) : run_mass_simt<float>(a, s);
 }
 

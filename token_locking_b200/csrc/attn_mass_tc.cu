@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
   const uint32_t tmem_base = *tmem_slot;
 
   // every role walks the same pieces, and in them the same (K/V head, block)s
-  const int W = pl.wbase[pl.njobs];
-  int w = (int)min((long long)blockIdx.x * pl.chunk, (long long)W), job = 0;
-  const int w_end = (int)min((long long)w + pl.chunk, (long long)W);
+  int w = kp_bound(pl, blockIdx.x, lane);
+  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
+  int job = kp_job_at(pl, pl.wbase, w, lane);
   KeyPiece pc{};
   int st = 0;                                 // Q stage
   uint32_t ph = 0;
@@ -410,6 +410,7 @@ cudaError_t key_mass_tc_setup(int D) {
 cudaError_t launch_key_mass_tc(KeyArgs a, cudaStream_t s) {
   a.ov = 1;
   a.min_chunk = 2;
+  a.join_cost = 0;
   return a.D == 128 ? run_mass_tc<128>(a, s) : run_mass_tc<64>(a, s);
 }
 

@@ -245,6 +245,7 @@ struct KeyArgs {
   float *mass, decay;
   float *ws;                      // key_attn_ws_floats / key_mass_ws_floats
   int ov, min_chunk;              // a unit's start-up and epilogue, least share of a CTA: tile times
+  int join_cost;                  // what a join costs a launch, in tile times
   int *plan;                      // KEY_PLAN_WORDS, the first kernel's plan for the second
   int n_ctas;                     // CTAs of the launch (attention / weight)
   int *err;

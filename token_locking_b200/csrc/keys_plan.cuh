@@ -24,7 +24,8 @@ struct KeyPlan {
   int kl[SL_MAX_BATCH];       // keys of each sequence's set, in [0, n_ctx]
   int wbase[KP_JOBS + 1];     // first virtual tile of each job; from [njobs] W
   int T[KP_JOBS];             // inner tiles of a unit of the job
-  int njobs, stacked, chunk, ov, empty;   // empty: some sequence has rows and no keys
+  int ubase[KP_JOBS + 1];     // first unit of each job, counted over all; from [njobs] their number
+  int njobs, stacked, chunk, per, ov, empty;   // empty: some sequence has rows and no keys
 };
 
 // One piece of a unit, as one CTA computes it.
@@ -97,8 +98,9 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
   const bool empty = __any_sync(0xffffffffu, (u0 > 0 && tp + t0 == 0) || (u1 > 0 && tp + t1 == 0));
   const int nu_p = kp_tiles(rows, uq);
   if (a.stack && tp > 0) {
-    const int cat = warp_sum_i(u0 * (tp + t0 + ov) + u1 * (tp + t1 + ov));
-    const int own = warp_sum_i((t0 > 0 ? u0 * (t0 + ov) : 0) + (t1 > 0 ? u1 * (t1 + ov) : 0));
+    const int cat = __reduce_add_sync(0xffffffffu, u0 * (tp + t0 + ov) + u1 * (tp + t1 + ov));
+    const int own = __reduce_add_sync(
+        0xffffffffu, (t0 > 0 ? u0 * (t0 + ov) : 0) + (t1 > 0 ? u1 * (t1 + ov) : 0));
     // the joined layout reads the prefix once per block of rows of any
     // sequence, but each row's two partial results pass through memory
     const int once = nu_p * (tp + ov) + own;
@@ -109,28 +111,40 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
   const int sh = stacked ? 1 : 0;
   const int T0 = weight ? u0 * a.Hkv : (stacked ? 0 : tp) + t0;
   const int T1 = weight ? u1 * a.Hkv : (stacked ? 0 : tp) + t1;
-  const int c0 = T0 > 0 ? (weight ? t0 : u0 * a.Hkv) * (T0 + ov) : 0;
-  const int c1 = T1 > 0 ? (weight ? t1 : u1 * a.Hkv) * (T1 + ov) : 0;
-  const int cp = stacked ? nu_p * a.Hkv * (tp + ov) : 0;
+  const int x0 = T0 > 0 ? (weight ? t0 : u0 * a.Hkv) : 0, c0 = x0 * (T0 + ov);
+  const int x1 = T1 > 0 ? (weight ? t1 : u1 * a.Hkv) : 0, c1 = x1 * (T1 + ov);
+  const int xp = stacked ? nu_p * a.Hkv : 0, cp = xp * (tp + ov);
   const int i0 = warp_incl_sum(c0, lane), i1 = warp_incl_sum(c1, lane);
   const int half = cp + __shfl_sync(0xffffffffu, i0, 31);
   const int W = half + __shfl_sync(0xffffffffu, i1, 31);
   pl.T[b0 + sh] = T0;
   pl.T[b1 + sh] = T1;
+  // the same in units, and the longest of them
+  const int y0 = warp_incl_sum(x0, lane), y1 = warp_incl_sum(x1, lane);
+  const int uhalf = xp + __shfl_sync(0xffffffffu, y0, 31);
+  const int U = uhalf + __shfl_sync(0xffffffffu, y1, 31);
+  const int longest = ov + __reduce_max_sync(
+      0xffffffffu, max(stacked ? tp : 0, max(x0 > 0 ? T0 : 0, x1 > 0 ? T1 : 0)));
+  const int share = (W + n_ctas - 1) / n_ctas, per = (U + n_ctas - 1) / n_ctas;
+  pl.ubase[b0 + sh] = xp + y0 - x0;
+  pl.ubase[b1 + sh] = uhalf + y1 - x1;
   pl.wbase[b0 + sh] = cp + i0 - c0;
   pl.wbase[b1 + sh] = half + i1 - c1;
   if (lane == 0) {
     if (stacked) {
       pl.T[0] = tp;
-      pl.wbase[0] = 0;
+      pl.wbase[0] = pl.ubase[0] = 0;
     }
     pl.q0[64] = ve;
     pl.wbase[64 + sh] = W;
+    pl.ubase[64 + sh] = U;
     pl.njobs = B + sh;
     pl.stacked = stacked;
     pl.ov = ov;
     pl.empty = empty;
-    pl.chunk = max((W + n_ctas - 1) / n_ctas, a.min_chunk);
+    pl.chunk = max(share, a.min_chunk);
+    // (a joint prefix passes every row through memory either way)
+    pl.per = (long long)per * longest <= share + (stacked ? 0 : a.join_cost) ? per : 0;
   }
   __syncwarp();
 }
@@ -149,12 +163,30 @@ __device__ __forceinline__ void key_plan_fetch(KeyPlan &pl, const int *from, int
 // Sequence of job j, or -1 for the shared prefix's job.
 __device__ __forceinline__ int kp_seq(const KeyPlan &pl, int j) { return pl.stacked ? j - 1 : j; }
 
+// The job whose virtual tiles (or units) hold `at` (all lanes of a warp).
+__device__ __forceinline__ int kp_job_at(const KeyPlan &pl, const int *base, int at, int lane) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < KP_JOBS; i += 32)
+    n += __popc(__ballot_sync(0xffffffffu, i + lane < pl.njobs && at >= base[min(i + lane + 1, KP_JOBS)]));
+  return min(n, pl.njobs - 1);
+}
+
+// The first virtual tile of CTA c's share.
+__device__ __forceinline__ int kp_bound(const KeyPlan &pl, int c, int lane) {
+  const int W = pl.wbase[pl.njobs];
+  if (!pl.per) return (int)min((long long)c * pl.chunk, (long long)W);
+  const int u = (int)min((long long)c * pl.per, (long long)pl.ubase[pl.njobs]);
+  if (u >= pl.ubase[pl.njobs]) return W;
+  const int j = kp_job_at(pl, pl.ubase, u, lane);
+  return pl.wbase[j] + (u - pl.ubase[j]) * (pl.T[j] + pl.ov);
+}
+
 // The piece of the unit at virtual tile w that ends at or before w_end; w moves
 // to its end.  False once nothing is left; pieces without inner tiles (a cut
 // inside the start-up share) are passed over.
 __device__ __forceinline__ bool key_next(const KeyPlan &pl, int heads, int &w, int w_end, int &job,
                                          KeyPiece &p) {
-  w_end = min(w_end, pl.wbase[pl.njobs]);
   while (w < w_end) {
     while (w >= pl.wbase[job + 1]) ++job;
     const int T = pl.T[job], cu = T + pl.ov;
@@ -177,9 +209,39 @@ __device__ __forceinline__ bool key_next(const KeyPlan &pl, int heads, int &w, i
 // Slot of a CTA's piece that does not cover its unit.
 __device__ __forceinline__ int kp_slot(int cta, int t0) { return 2 * cta + (t0 > 0 ? 0 : 1); }
 
-// The CTAs whose shares meet a unit, and the tiles of CTA c's piece of it.
+// Division by a number that is known before many of them: n / d for 0 <= n < 2^31.
+// With s = ceil(log2 d) - 1 and m = ceil(2^(32 + s) / d) < 2^32, m d exceeds
+// 2^(32 + s) by less than d <= 2^(s + 1), so n m / 2^(32 + s) is too large by less
+// than n / 2^31 / d < 1 / d, and its whole part is that of n / d.
+struct FastDiv {
+  uint32_t m;
+  int s;                      // -1: d = 1
+  __host__ __device__ static FastDiv of(int d) {
+    FastDiv f{0u, -1};
+    while ((2ll << f.s + 1) < 2ll * d) ++f.s;
+    if (f.s >= 0) f.m = (uint32_t)(((1ull << (32 + f.s)) + d - 1) / d);
+    return f;
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return s < 0 ? n : (int)(__umulhi((uint32_t)n, m) >> s);
+  }
+};
+
+// The shares that meet a unit of T tiles: the first, the last, and CTA c's tiles
+// of it.
+__device__ __forceinline__ int kp_first(const KeyPlan &pl, FastDiv chunk, int w_unit) {
+  return pl.per ? 0 : chunk.div(w_unit);
+}
+__device__ __forceinline__ int kp_last(const KeyPlan &pl, FastDiv chunk, int w_unit, int T) {
+  return pl.per ? 0 : chunk.div(w_unit + T + pl.ov - 1);
+}
 __device__ __forceinline__ void kp_piece_of(const KeyPlan &pl, int w_unit, int T, int c, int &t0,
                                             int &t1) {
+  if (pl.per) {
+    t0 = 0;
+    t1 = T;
+    return;
+  }
   const int v0 = max(c * pl.chunk, w_unit) - w_unit;
   const int v1 = min((long long)(c + 1) * pl.chunk, (long long)w_unit + T + pl.ov) - w_unit;
   t0 = max(0, v0 - pl.ov);
