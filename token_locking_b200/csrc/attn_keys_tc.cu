@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         __syncwarp();
         if (lane == 0) mbar_arrive(tbar(j, 1));
         if (nv < BN) {
+          key_cold();
 #pragma unroll
           for (int i = 0; i < HB; ++i) s[i] = half * HB + i < nv ? s[i] : -INFINITY;
         }
@@ -423,17 +424,21 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         const float m_use = (first || resc) ? m_new : m;
         const float alpha = resc ? (m == -INFINITY ? 0.f : ex2_approx(m - m_new)) : 1.f;
         const float m_sub = m_use == -INFINITY ? 0.f : -m_use;  // all scores -inf: p = 0
-        float sa[4] = {0.f, 0.f, 0.f, 0.f};
+        f32x2 sa[2] = {0ull, 0ull};
+        const f32x2 cc = pack2(c2, c2), mm = pack2(m_sub, m_sub);
         uint32_t pk[HB / 2];
 #pragma unroll
         for (int i = 0; i < HB; i += 2) {
-          fma2(s[i], s[i + 1], c2, m_sub);
-          s[i] = ex2_approx(s[i]);
-          s[i + 1] = ex2_approx(s[i + 1]);
-          add2(sa[i & 2], sa[(i & 2) + 1], s[i], s[i + 1]);
-          pk[i / 2] = kc_pack(s[i], s[i + 1]);
+          float x, y;
+          unpack2(fma2(pack2(s[i], s[i + 1]), cc, mm), x, y);
+          x = ex2_approx(x);
+          y = ex2_approx(y);
+          sa[i >> 1 & 1] = add2(sa[i >> 1 & 1], pack2(x, y));
+          pk[i / 2] = kc_pack(x, y);
         }
-        l = l * alpha + ((sa[0] + sa[1]) + (sa[2] + sa[3]));
+        float l0, l1;
+        unpack2(add2(sa[0], sa[1]), l0, l1);
+        l = l * alpha + (l0 + l1);
         m = m_use;
         // the last P V product has read P and written O
         if (!first) wait(3, (cs & 1u) ^ 1u);

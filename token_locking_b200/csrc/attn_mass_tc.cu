@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
     const int quarter = warp & 3;
     const uint32_t t_s = tmem_base + ((uint32_t)(quarter * 32) << 16) + 2 * j * 128 + half * KM_HALF;
     const float c2 = a.scale * KEY_LOG2E;
+    const f32x2 cc = pack2(c2, c2);
     uint32_t cs = 0;
     while (ok && key_next(pl, 1, w, w_end, job, pc)) {
       const int b = pc.job, i0 = pc.unit * KM_KEYS + j * 128 + quarter * 32 + lane;
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
       const int n_last = (qn - (nqt - 1) * QR) * a.G;    // packed rows of the last block
       const int n_full = QR * a.G;
       int blk = pc.t0 % nqt;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      f32x2 sum[2] = {0ull, 0ull};
       for (int t = pc.t0; t < pc.t1; ++t) {
         ok = key_wait(bar(C::B_F + st), ph, abort_flag, lim);
         if (!ok) break;
@@ -319,8 +320,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
           ok = key_wait(tfull(j, u), (cs >> 1) & 1u, abort_flag, lim);
           if (!ok) break;
           tc_fence_after();
-          const float4 *nl = reinterpret_cast<const float4 *>(smem + C::Q_OFF + st * C::STAGE +
-                                                              C::TILE) + half * (KM_HALF / 4);
+          const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(
+              smem + C::Q_OFF + st * C::STAGE + C::TILE) + half * (KM_HALF / 4);
           const int nv = (blk + 1 == nqt ? n_last : n_full) - half * KM_HALF;
 #pragma unroll
           for (int c = 0; c < KM_HALF; c += 32) {
@@ -331,20 +332,21 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
               __syncwarp();
               if (lane == 0) mbar_arrive(tfree(j, u));
             }
+            if (nv < KM_HALF) {               // rows that are not there may hold anything
+              key_cold();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = c + i < nv ? s[i] : -INFINITY;
+            }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 x = nl[(c + i) / 4];
-              fma2v(s[i], s[i + 1], c2, x.x, x.y);
-              fma2v(s[i + 2], s[i + 3], c2, x.z, x.w);
+              const ulonglong2 x = nl[(c + i) / 4];
+              float p[4];
+              unpack2(fma2(pack2(s[i], s[i + 1]), cc, x.x), p[0], p[1]);
+              unpack2(fma2(pack2(s[i + 2], s[i + 3]), cc, x.y), p[2], p[3]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[i + e] = ex2_approx(s[i + e]);
-              // rows that are not there may hold anything
-              if (nv < KM_HALF) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[i + e] = c + i + e < nv ? s[i + e] : 0.f;
-              }
-              add2(sum[0], sum[1], s[i], s[i + 1]);
-              add2(sum[2], sum[3], s[i + 2], s[i + 3]);
+              for (int e = 0; e < 4; ++e) p[e] = ex2_approx(p[e]);
+              sum[0] = add2(sum[0], pack2(p[0], p[1]));
+              sum[1] = add2(sum[1], pack2(p[2], p[3]));
             }
           }
           ++cs;
@@ -355,7 +357,9 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
         next_stage();
       }
       if (ok && mine && i0 < pl.kl[b]) {
-        const float v = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float v0, v1;
+        unpack2(add2(sum[0], sum[1]), v0, v1);
+        const float v = v0 + v1;
         const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
         const size_t n_slots = 2 * (size_t)a.n_ctas * 2 * KM_KEYS;
         a.ws[whole ? n_slots + (size_t)half * a.batch * a.n_ctx + (size_t)b * a.n_ctx + i0

@@ -300,23 +300,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ void fma2(float &x, float &y, float a, float b) {   // x = x a + b, ...
-  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n"
-      " mov.b64 r, {%3, %3};\n fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}\n"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
+typedef unsigned long long f32x2;             // a pair of floats in two registers
+__device__ __forceinline__ f32x2 pack2(float x, float y) {
+  f32x2 p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
 }
-__device__ __forceinline__ void fma2v(float &x, float &y, float a, float b, float c) {
-  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %2};\n"       // x = x a + b
-      " mov.b64 r, {%3, %4};\n fma.rn.f32x2 p, p, q, r;\n mov.b64 {%0, %1}, p;\n}\n"   // y = y a + c
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b), "f"(c));
+__device__ __forceinline__ void unpack2(f32x2 p, float &x, float &y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
 }
-__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {   // x += a, y += b
-  asm("{\n .reg .b64 p, q;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n"
-      " add.rn.f32x2 p, p, q;\n mov.b64 {%0, %1}, p;\n}\n"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(b));
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 // 2^x on the SFU (approximate, flush-to-zero; 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {
