@@ -54,6 +54,12 @@ SHAPES = [
     ("f32", [1] * 6, [9] * 6, 12, 4, 2, 32, 333, False),
     ("f32", [100, 20], [128, 300], 300, 3, 1, 128, 65, True),
     ("f32", [10], [40], 40, 2, 1, 4, 0, False),
+    # more units than CTAs, shares of whole ones; joint prefix over many rows, joined in fours
+    ("bf16", [600, 550], [200, 170], 210, 32, 32, 128, 0, True),
+    ("bf16", [300, 700], [96, 300], 300, 64, 64, 64, 0, False),
+    ("bf16", [24, 5, 30, 1, 0, 41, 24, 24, 63, 24, 2, 50], [100] * 11 + [0], 120, 16, 16, 128, 900, False),
+    ("bf16", [7, 40, 90], [64, 0, 500], 500, 48, 3, 64, 3001, True),
+    ("f32", [200, 190, 64, 70], [100, 64, 129, 30], 130, 16, 16, 64, 70, True),
 ]
 
 
@@ -125,6 +131,126 @@ def test_no_lengths_and_another_scale(cuda_dev, dtype, dh):
     o2, _ = c.outputs()
     ka.attend(c.q, c.k, c.v, o2, c.seq_off)
     assert torch.equal(o, o2)
+
+
+KERNELS = [("bf16", 128), ("bf16", 64), ("bf16", 96), ("f32", 64)]
+
+
+@pytest.mark.parametrize("dtype,dh", KERNELS)
+def test_scores_far_apart(cuda_dev, dtype, dh):
+    """Scores in the hundreds: the maximum rises by more than 2^8 between tiles
+    and one key takes nearly all of a row's weight."""
+    c = Case(cuda_dev, dtype, [70, 3], [400, 333], 400, 4, 2, dh, prefix=150, seed=31, spread=30.0)
+    # later keys are longer, so that the running maximum keeps rising
+    ramp = torch.linspace(0.1, 4.0, 400, device=cuda_dev).repeat(2)[:, None]
+    c.k.copy_((c.k.float() * ramp).to(c.dt))
+    ka = c.key_attention()
+    o, lse = c.outputs()
+    c.attend(ka, o, lse)
+    _check_attend(c, o, lse)
+    mass = torch.empty((2, 400), device=cuda_dev)
+    ka.mass(c.q, c.k, lse, mass, c.seq_off, key_len=c.key_len)
+    want, bound = ref_mass(c, lse)
+    assert float(((mass.double() - want).abs() - bound).max()) <= 0
+
+
+@pytest.mark.parametrize("dtype,dh", KERNELS)
+def test_infinite_scores_and_nan_stay_in_their_rows(cuda_dev, dtype, dh):
+    """Keys of -inf score weigh nothing, a row of them alone gives 0 and -inf, and a
+    NaN query spoils its own row of attention only (and the weights it adds to)."""
+    c = Case(cuda_dev, dtype, [40, 30], [130, 90], 200, 2, 1, dh, seed=33)
+    H = c.H
+    q = c.q.abs() + 0.1                                  # positive: the score's sign is the key's
+    c.q.copy_(q.to(c.dt))
+    c.k[5], c.k[77] = -math.inf, -math.inf               # two keys of sequence 0
+    c.k[200:290] = -math.inf                             # all of sequence 1's
+    c.q[3] = float("nan")
+    ka = c.key_attention()
+    o, lse = c.outputs()
+    c.attend(ka, o, lse)
+    assert torch.isnan(o[3]).all() and torch.isnan(lse[3]).all()
+    assert (o[40:70] == 0).all() and (lse[40:70] == -math.inf).all()
+    clean = [r for r in range(40) if r != 3]
+    assert torch.isfinite(o[clean]).all() and torch.isfinite(lse[clean]).all()
+    live = [i for i in range(130) if i not in (5, 77)]
+    s = 1.0 / math.sqrt(dh)
+    for h in range(H):
+        z = c.q[clean, h * dh:(h + 1) * dh].double() @ c.k[live].double().T * s
+        assert torch.allclose(lse[clean, h].double(), torch.logsumexp(z, dim=1), atol=1e-4, rtol=1e-5)
+    # without the NaN row the weights are finite, and zero for the -inf keys
+    mass = torch.empty((2, 200), device=cuda_dev)
+    ka.mass(c.q[4:], c.k, lse[4:].contiguous(), mass,
+            torch.tensor([0, 36, 66], dtype=torch.int32, device=cuda_dev), key_len=c.key_len)
+    assert torch.isfinite(mass).all() and (mass[0, [5, 77]] == 0).all() and (mass[1] == 0).all()
+    ka.mass(c.q, c.k, lse, mass, c.seq_off, key_len=c.key_len)
+    assert torch.isnan(mass[0, live]).all() and (mass[1] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,dh", KERNELS)
+def test_no_rows(cuda_dev, dtype, dh):
+    """No rows at all: nothing attends, the weights only decay."""
+    c = Case(cuda_dev, dtype, [0, 0], [9, 4], 12, 2, 1, dh, prefix=5, seed=35)
+    ka = c.key_attention()
+    o, lse = c.outputs()
+    c.attend(ka, o, lse)
+    prev = torch.rand((2, 12), device=cuda_dev)
+    mass = torch.full_like(prev, float("nan"))
+    ka.mass(c.q, c.k, lse, mass, c.seq_off, key_len=c.key_len, mass_prev=prev, decay=0.25)
+    assert torch.equal(mass, prev * 0.25)
+    ka.mass(c.q, c.k, lse, mass, c.seq_off, key_len=c.key_len)
+    assert (mass == 0).all()
+
+
+@pytest.mark.parametrize("dtype,dh", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_groups_up_to_sixty_four(cuda_dev, dtype, dh):
+    for G in (3, 5, 31, 33, 64):
+        c = Case(cuda_dev, dtype, [9, 1, 20], [70, 33, 128], 130, 2 * G, 2, dh, prefix=90, seed=G)
+        c.poison()
+        ka = c.key_attention()
+        o, lse = c.outputs()
+        c.attend(ka, o, lse)
+        _check_attend(c, o, lse)
+        mass = torch.empty((3, 130), device=cuda_dev)
+        ka.mass(c.q, c.k, lse, mass, c.seq_off, key_len=c.key_len)
+        want, bound = ref_mass(c, lse)
+        assert float(((mass.double() - want).abs() - bound).max()) <= 0
+
+
+def test_alignment_of_sixteen_bytes(cuda_dev):
+    """Operands and results on 16-byte boundaries that are no 32-byte ones."""
+    c = Case(cuda_dev, "bf16", [150, 20], [200, 100], 200, 2, 2, 128, seed=37, pad=8)
+    for n in ("q", "k", "v"):
+        t = getattr(c, n)
+        big = torch.full((t.shape[0], t.shape[1] + 24), float("nan"), dtype=t.dtype, device=cuda_dev)
+        big[:, 8:8 + t.shape[1]] = t
+        setattr(c, n, big[:, 8:8 + t.shape[1]])
+    ka = c.key_attention()
+    buf = torch.full((c.rows, 256 + 24), 7.0, dtype=c.dt, device=cuda_dev)
+    o, lse = buf[:, 8:264], c.outputs()[1]
+    c.attend(ka, o, lse)
+    _check_attend(c, o, lse)
+    assert (buf[:, :8] == 7).all() and (buf[:, 264:] == 7).all()
+
+
+def test_streams_one_after_the_other(cuda_dev):
+    """One object used from two streams that the caller orders, and its result read
+    on a third."""
+    c = Case(cuda_dev, "bf16", [90, 40], [700, 300], 700, 4, 4, 128, prefix=333, seed=39)
+    ka = c.key_attention()
+    outs = [c.outputs() for _ in range(4)]
+    ss = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    last = None
+    for i, (o, lse) in enumerate(outs):
+        s = ss[i % 2]
+        if last is not None:
+            s.wait_event(last)
+        c.attend(ka, o, lse, stream=s)
+        last = torch.cuda.Event()
+        last.record(s)
+    torch.cuda.current_stream().wait_event(last)
+    for o, lse in outs:
+        _check_attend(c, o, lse)
 
 
 @pytest.mark.parametrize("dtype,dh", [("bf16", 128), ("f32", 32)])
