@@ -65,7 +65,7 @@ struct EvShared {
   int wsum[EV_WARPS], wsum2[EV_WARPS];
   int fixed, cand;                           // of this CTA's entries
   int above, equal;                          // of this CTA's: kept for certain, at the threshold
-  int digit, rank;
+  int digit, rank, count;                    // of the bin that holds the threshold
 };
 }  // namespace
 
@@ -171,15 +171,23 @@ __global__ void __launch_bounds__(EV_THREADS) evict_kernel(
           const bool low = rest >= excl + h1;
           sh.digit = low ? d - 1 : d;
           sh.rank = rest - excl - (low ? h1 : 0);
+          sh.count = low ? h0 : h1;
         }
       }
       __syncthreads();
       prefix |= (uint32_t)sh.digit << shift;
       rank = sh.rank;
+      const bool all = rank + 1 == sh.count;
       __syncthreads();
+      if (all) {
+        // the whole bin stays: everything from its first weight on, no ties
+        // left to settle (mostly so after two passes)
+        thr = prefix - 1;
+        break;
+      }
+      thr = prefix;
+      ties = pass == 2 ? rank + 1 : 0;
     }
-    thr = prefix;
-    ties = rank + 1;
   }
   // a warp's run of this CTA's entries: how many are kept for certain, and how
   // many equal the threshold
