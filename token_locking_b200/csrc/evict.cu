@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_kernel(
       if (pass > 0) {
         const uint32_t pmask = pass == 1 ? 0xffe00000u : 0xfffffc00u;
         const uint32_t dmask = pass == 1 ? 0x7ffu : 0x3ffu;
+#pragma unroll 4
         for (int i = tid; i < n; i += EV_THREADS) {
           const uint32_t k = key(i);
           if (candidate(k) && (k & pmask) == prefix)
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_kernel(
   auto above = [&](uint32_t k) { return k != EV_ABSENT && (k == EV_FIXED || k > thr); };
   auto equal = [&](uint32_t k) { return k == thr && candidate(k); };
   int ca = 0, ce = 0;
+#pragma unroll 4
   for (int i = i0 + lane; i < i1; i += 32) {
     const uint32_t k = key(i);
     ca += above(k);
@@ -234,6 +236,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_kernel(
   out += min(seen, ties);
   // stable write: entries above thr, and the first `ties` equal to it
   const unsigned int below = (1u << lane) - 1u;
+#pragma unroll 4
   for (int i = i0; i < i1; i += 32) {
     const uint32_t k = i + lane < i1 ? key(i + lane) : EV_ABSENT;
     const bool eq = equal(k);
