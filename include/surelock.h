@@ -488,8 +488,8 @@ typedef struct sl_key_set {
  * row's key set.  q, o: [rows][ld >= n_heads * head_dim]; k, v:
  * [batch * n_ctx][ld_kv >= n_kv_heads * head_dim]; prefix: [prefix_len][ld_prefix];
  * pointers and rows 16-byte aligned.  d_lse [rows][n_heads] fp32, or NULL.  A row
- * without keys gets o = 0, lse = -inf; rows outside every sequence are not
- * written, and entries outside a key set are never read into a result.  o and
+ * without keys, or with scores of -inf only, gets o = 0, lse = -inf; rows outside
+ * every sequence are not written, and entries outside a key set never reach a result.  o and
  * lse must not overlap the operands.  Softmax and sums in fp32; bf16 operands
  * round p to bf16 for the product with v. */
 sl_status sl_key_attention(sl_key_attn *a, int rows, const void *d_q, int64_t ld_q,
@@ -501,7 +501,9 @@ sl_status sl_key_attention(sl_key_attn *a, int rows, const void *d_q, int64_t ld
  * sl_key_attention left for these rows (prefix included): the attention weight
  * each cached entry received, to be accumulated over layers and steps.  mass and
  * mass_prev: [batch][n_ctx] fp32, may be the same; decay = 0 does not read
- * mass_prev (may be NULL).  Rows with lse = -inf weigh nothing. */
+ * mass_prev (may be NULL).  Rows with lse = -inf weigh nothing.  The same call gives
+ * the same bits, unless a list names a position more than once (its weights are
+ * then added in no fixed order). */
 sl_status sl_key_mass(sl_key_attn *a, int rows, const void *d_q, int64_t ld_q, const void *d_k,
                       int64_t ld_kv, const sl_key_set *set, const float *d_lse, float decay,
                       const float *d_mass_prev, float *d_mass, void *stream);
@@ -537,8 +539,8 @@ sl_status sl_timing_enable(sl_model *m, int enable);
 sl_status sl_timing_read(sl_model *m, sl_timing *out, int reset);
 
 /* Device error word, set by a kernel that gave up a bounded wait or met a
- * token id outside [0, vocab) (that row is embedded as zeros, never read from
- * out of range): returns SL_ERR_TIMEOUT or SL_ERR_STATE respectively (and
+ * token id outside [0, vocab) or a listed key position outside [0, n_ctx) (that
+ * row is embedded, that key taken, as zeros, never read from out of range): returns SL_ERR_TIMEOUT or SL_ERR_STATE respectively (and
  * clears the word if `clear`), SL_OK if nothing was recorded.  Synchronises
  * the device. */
 sl_status sl_device_check(int clear);

@@ -362,7 +362,8 @@ extern "C" sl_status sl_device_check(int clear) {
     if (clear) SL_CUDA(cudaMemset(w, 0, sizeof(int)));
     if (v >= 1 && v <= 3) return fail(SL_ERR_TIMEOUT, "a kernel gave up a bounded wait (code %d)", v);
     if (v == DEV_BAD_INDEX)
-      return fail(SL_ERR_STATE, "a kernel met a token id outside [0, vocab) and skipped it");
+      return fail(SL_ERR_STATE, "a kernel met a token id outside [0, vocab) or a key "
+                  "position outside [0, n_ctx) and skipped it");
     return fail(SL_ERR_CUDA, "a kernel reported device error %d", v);
   }
   return SL_OK;

@@ -13,6 +13,11 @@
 // of CTAs takes one sequence, each a run of its entries: histograms and counts
 // are summed over the cluster through distributed shared memory, whole numbers
 // in a fixed order, so the result is exact and the same every time.
+//
+// Bound by latency: 4 x 2048 entries take 9.2 us, 4 x 131072 take 22 us (their
+// bytes 0.6 us), of which 5 us are the second and third pass and about 6 us the
+// first pass's loads and histogram.  Eight loads in flight a thread instead of
+// four, ahead of the histogram: 0.7 us more.
 #include "common.cuh"
 #include "internal.h"
 
