@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
   const int rn = min(uq, pl.q0[j + 1] - r0) * a.G;
   const int y = k * gridDim.y + blockIdx.y, n_y = n_cuts * gridDim.y;   // this block of the unit's
   const int nw = join_warps(rn, (long long)KJ_WARPS * n_y), sub = warp % nw, per = KJ_WARPS / nw;
-  if (nw > 1) {
+  if (nw > 1 || rn <= 2 * KJ_WARPS * n_y) {   // few rows a warp: four pieces in flight
     for (int i0 = y * per; i0 < rn; i0 += n_y * per) {
       const int r = i0 + warp / nw;
       const bool there = r < rn;
