@@ -29,7 +29,8 @@ constexpr int KS_THREADS = 256;
 // 256 threads as 16 x 16: thread (ty, tx) holds scores of rows 4 ty + i and
 // keys tx + 16 j, and of the output rows 4 ty + i the columns 4 tx + 64 c.
 // Operands are staged in shared memory as fp32 with rows padded by four floats
-// (16 rows read at a time then fall into distinct banks).  Bound by shared
+// (16 rows read at a time then fall into distinct banks), four threads a row, a
+// key's position read a tile ahead.  Bound by shared
 // memory reads (8 16-byte reads per 64 multiply-adds), and in small calls by
 // latency: 200 and 101 rows of 8 heads of 64 over 192 and 96 keys take 27 us with
 // shares of one tile, 42 us with shares of four.
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
   if (blockIdx.x == 0) key_plan_publish(pl, a.plan, tid, KS_THREADS);
   pdl_trigger();
   const int tp = kp_tiles(a.prefix_len, KS_T);
-  const int d4 = D >> 2;
+  const int lr = tid >> 2, lc = (tid & 3) * 4;      // row and first column this thread stages
   const float c2 = a.scale * KEY_LOG2E;
 
   int w = kp_bound(pl, blockIdx.x, lane);
@@ -61,13 +62,22 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
     const int r0 = (b < 0 ? pl.q0[0] : pl.q0[b]) + pc.unit * QR;
     const int rn = min(QR, (b < 0 ? pl.q0[a.batch] : pl.q0[b + 1]) - r0) * a.G;   // packed rows
     __syncthreads();
-    for (int i = tid; i < KS_T * d4; i += KS_THREADS) {
-      const int r = i / d4, c = (i - r * d4) * 4;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < rn)
-        v = load4((const T *)a.q + (r0 + r / a.G) * a.ld_q + (pc.hk * a.G + r % a.G) * D + c);
-      *reinterpret_cast<float4 *>(sq + r * ld + c) = v;
+    {
+      const int g = lr / a.G;
+      const T *src = (const T *)a.q + (r0 + g) * a.ld_q + (pc.hk * a.G + lr - g * a.G) * D;
+#pragma unroll 4
+      for (int c = lc; c < D; c += 16)
+        *reinterpret_cast<float4 *>(sq + lr * ld + c) =
+            lr < rn ? load4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    // cache position of this thread's key of tile t, -1 where there is none
+    auto entry = [&](int t) {
+      const bool pre = b < 0 || (!pl.stacked && t < tp);
+      const int i = (pre || pl.stacked ? t : t - tp) * KS_T + lr;
+      if (t >= pc.t1 || i >= (pre ? a.prefix_len : pl.kl[b])) return -1;
+      return pre ? i : key_pos(a, b, i);
+    };
+    int nxt = entry(pc.t0);
     float m[4], l[4];
     float4 acc[4][2];
 #pragma unroll
@@ -81,22 +91,22 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
       const bool pre = b < 0 || (!pl.stacked && t < tp);
       const int i0 = (pre || pl.stacked ? t : t - tp) * KS_T;
       const int nv = min(KS_T, (pre ? a.prefix_len : pl.kl[b]) - i0);
+      const int pos = nxt;
+      const long long off = pre ? pos * a.ld_p + pc.hk * D
+                                : ((long long)b * a.n_ctx + pos) * a.ld_kv + pc.hk * D;
+      const T *kr = (const T *)(pre ? a.kp : a.k) + off, *vr = (const T *)(pre ? a.vp : a.v) + off;
       __syncthreads();
-      for (int i = tid; i < KS_T * d4; i += KS_THREADS) {
-        const int r = i / d4, c = (i - r * d4) * 4;
+#pragma unroll 4
+      for (int c = lc; c < D; c += 16) {
         float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-        if (r < nv) {
-          const int pos = pre ? i0 + r : key_pos(a, b, i0 + r);
-          if (pos >= 0) {
-            const long long off = pre ? pos * a.ld_p + pc.hk * D + c
-                                      : ((long long)b * a.n_ctx + pos) * a.ld_kv + pc.hk * D + c;
-            kv = load4((const T *)(pre ? a.kp : a.k) + off);
-            vv = load4((const T *)(pre ? a.vp : a.v) + off);
-          }
+        if (pos >= 0) {
+          kv = load4(kr + c);
+          vv = load4(vr + c);
         }
-        *reinterpret_cast<float4 *>(sk + r * ld + c) = kv;
-        *reinterpret_cast<float4 *>(sv + r * ld + c) = vv;
+        *reinterpret_cast<float4 *>(sk + lr * ld + c) = kv;
+        *reinterpret_cast<float4 *>(sv + lr * ld + c) = vv;
       }
+      nxt = entry(t + 1);
       __syncthreads();
       float s[4][4] = {};
       for (int c = 0; c < D; c += 4) {

@@ -30,9 +30,10 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   __shared__ KeyPlan pl;
   __shared__ float sL[MS_T], red[MS_THREADS / 16][MS_T];
   float *smem = reinterpret_cast<float *>(ms_smem4);
-  const int D = a.D, ld = D + 4, d4 = D >> 2;
+  const int D = a.D, ld = D + 4;
   float *sq = smem, *sk = sq + MS_T * ld;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, lane = tid & 31;
+  const int lr = tid >> 2, lc = (tid & 3) * 4;      // row and first column this thread stages
   const int QR = MS_T / a.G;
   pdl_wait();
   if (tid < 32) key_plan_build(pl, a, QR, MS_T, gridDim.x, true, lane);
@@ -51,28 +52,26 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
     const int qn = pl.q0[b + 1] - pl.q0[b], nqt = kp_tiles(qn, QR);
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     int hk_staged = -1;
+    const int pos = lr < nv ? key_pos(a, b, i0 + lr) : -1;   // of the key this thread stages
     for (int t = pc.t0; t < pc.t1; ++t) {
       const int hk = t / nqt, r0 = pl.q0[b] + (t - hk * nqt) * QR;
       const int rn = min(QR, pl.q0[b + 1] - r0) * a.G;
       __syncthreads();
       if (hk != hk_staged) {
         hk_staged = hk;
-        for (int i = tid; i < MS_T * d4; i += MS_THREADS) {
-          const int r = i / d4, c = (i - r * d4) * 4;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < nv) {
-            const int pos = key_pos(a, b, i0 + r);
-            if (pos >= 0)
-              v = load4((const T *)a.k + ((long long)b * a.n_ctx + pos) * a.ld_kv + hk * D + c);
-          }
-          *reinterpret_cast<float4 *>(sk + r * ld + c) = v;
-        }
+        const T *src = (const T *)a.k + ((long long)b * a.n_ctx + pos) * a.ld_kv + hk * D;
+#pragma unroll 4
+        for (int c = lc; c < D; c += 16)
+          *reinterpret_cast<float4 *>(sk + lr * ld + c) =
+              pos >= 0 ? load4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      for (int i = tid; i < MS_T * d4; i += MS_THREADS) {
-        const int r = i / d4, c = (i - r * d4) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rn) v = load4((const T *)a.q + (r0 + r / a.G) * a.ld_q + (hk * a.G + r % a.G) * D + c);
-        *reinterpret_cast<float4 *>(sq + r * ld + c) = v;
+      {
+        const int g = lr / a.G;
+        const T *src = (const T *)a.q + (r0 + g) * a.ld_q + (hk * a.G + lr - g * a.G) * D;
+#pragma unroll 4
+        for (int c = lc; c < D; c += 16)
+          *reinterpret_cast<float4 *>(sq + lr * ld + c) =
+              lr < rn ? load4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       if (tid < MS_T) {
         // rows that are not there, or saw no key, weigh nothing
