@@ -30,10 +30,9 @@ constexpr int KS_THREADS = 256;
 // keys tx + 16 j, and of the output rows 4 ty + i the columns 4 tx + 64 c.
 // Operands are staged in shared memory as fp32 with rows padded by four floats
 // (16 rows read at a time then fall into distinct banks), four threads a row, a
-// key's position read a tile ahead.  Bound by shared
-// memory reads (8 16-byte reads per 64 multiply-adds), and in small calls by
-// latency: 200 and 101 rows of 8 heads of 64 over 192 and 96 keys take 27 us with
-// shares of one tile, 42 us with shares of four.
+// key's position read a tile ahead.  Bound by shared memory reads (8 16-byte reads
+// per 64 multiply-adds), and in small calls by latency: 200 and 159 rows of 8 heads
+// of 64 over 192 and 130 keys take 24 us with shares of one tile, 36 us of two.
 template <typename T>
 __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs a) {
   extern __shared__ float4 ks_smem4[];

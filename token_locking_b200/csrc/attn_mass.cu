@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
       }
       __syncthreads();
       float s[4][4] = {};
+#pragma unroll 4
       for (int c = 0; c < D; c += 4) {
         float4 x[4], y[4];
 #pragma unroll
