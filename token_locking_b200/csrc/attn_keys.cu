@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
   const int j = kp_job_at(pl, pl.wbase, (int)cut, lane);
   const int cu = pl.T[j] + pl.ov, u = ((int)cut - pl.wbase[j]) / cu;
   const int wu = pl.wbase[j] + u * cu;
-  if (cut == wu) return;                      // between two units
+  // between two units, or behind a job's last one
+  if (cut == wu || u >= pl.ubase[j + 1] - pl.ubase[j]) return;
   // its cuts share the rows: this is the k-th of n_cuts; none of them where all
   // its tiles lie in one share, which then wrote the rows
   const JoinUnit un(pl, chunk, j, wu);
