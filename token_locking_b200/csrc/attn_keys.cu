@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
   const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
   int job = kp_job_at(pl, pl.wbase, w, lane);
   KeyPiece pc;
-  while (key_next(pl, a.Hkv, w, w_end, job, pc)) {
+  while (key_next(pl, w, w_end, job, pc)) {
     const int b = kp_seq(pl, pc.job);
     const int r0 = (b < 0 ? pl.q0[0] : pl.q0[b]) + pc.unit * QR;
     const int rn = min(QR, (b < 0 ? pl.q0[a.batch] : pl.q0[b + 1]) - r0) * a.G;   // packed rows
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
           const int rb = row - pl.q0[b], up = by_uq.div(rp), ub = by_uq.div(rb);
           const JoinUnit p(pl, chunk, 0, pl.wbase[0] + (up * a.Hkv + hk) * (pl.T[0] + pl.ov));
           const JoinUnit o(pl, chunk, b + 1,
-                           pl.wbase[b + 1] + (ub * a.Hkv + hk) * (pl.T[b + 1] + pl.ov));
+                           pl.wbase[b + 1] + (hk * pl.nu[b + 1] + ub) * (pl.T[b + 1] + pl.ov));
           const int n = min(min(end, (up + 1) * uq) - rp, min(pl.q0[b + 1], pl.q0[b] + (ub + 1) * uq) - row);
           JoinAcc x[4] = {none, none, none, none};
           gather4(x, p, (rp - up * uq) * a.G + g, a.G, n, 0, row, h);
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
         while (pl.q0[b + 1] <= row) ++b;
         const int rb = row - pl.q0[b], up = by_uq.div(rp), ub = by_uq.div(rb);
         const JoinUnit p(pl, chunk, 0, pl.wbase[0] + (up * a.Hkv + hk) * (pl.T[0] + pl.ov));
-        const JoinUnit o(pl, chunk, b + 1, pl.wbase[b + 1] + (ub * a.Hkv + hk) * (pl.T[b + 1] + pl.ov));
+        const JoinUnit o(pl, chunk, b + 1, pl.wbase[b + 1] + (hk * pl.nu[b + 1] + ub) * (pl.T[b + 1] + pl.ov));
         const int r_p = (rp - up * uq) * a.G + g, r_o = (rb - ub * uq) * a.G + g;
         gather(x, p.n + o.n, sub, nw, [&](int e) {
           return e < p.n ? p.rec(pl, e, rt, r_p, key_rec_row(a, rt, 0, row, h))
@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(32 * KJ_WARPS, 4) key_join_kernel(const KeyArg
     if (t0 == 0 && t1 == pl.T[j]) return;
     t1 = max(t1, 0);
   }
-  const int unit = u / a.Hkv, hk = u - unit * a.Hkv;
+  int unit, hk;
+  kp_unit_of(pl, j, u, unit, hk);
   const int r0 = pl.q0[j] + unit * uq;
   const int rn = min(uq, pl.q0[j + 1] - r0) * a.G;
   const int y = k * gridDim.y + blockIdx.y, n_y = n_cuts * gridDim.y;   // this block of the unit's

@@ -72,7 +72,7 @@ template <int D, int BN> struct KcCfg {
   // row copies: 16-byte chunks of a row, rows of a warp instruction, instructions
   // of each of the two warps, tiles in flight
   static constexpr int CH = D / 8, RPI = 32 / CH, NI = BN / RPI / 2, LAG = 2;
-  static constexpr int PLAN_OFF = BAR_OFF + 512;
+  static constexpr int PLAN_OFF = BAR_OFF + 256;
   // TMEM columns: per row tile S, then P (two bf16 keys a column), from a
   // multiple of 64; then O of both
   static constexpr uint32_t T_COLS = (BN + BN / 2 + 63) / 64 * 64;
@@ -81,7 +81,7 @@ template <int D, int BN> struct KcCfg {
   static constexpr uint32_t L_COL = X_COL + 4;          // and row sums
   static_assert(O_COL + 2 * D <= 512 && L_COL + 2 <= T_COLS, "TMEM columns");
   static constexpr int HB = BN / 2;                     // keys of a softmax warpgroup
-  static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
+  static_assert(8 * B_COUNT + 8 <= 256 && sizeof(KeyPlan) <= TAIL - 256, "barriers and plan");
   static_assert(BN % (2 * RPI) == 0 && NI * RPI <= 64, "two rows a lane of a warp's share");
   static_assert(LAG < NP, "row copies in flight");
   static_assert(SMEM <= 232448 && BN % 16 == 0, "shared memory, key tile");
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     int st = 0, np = 0;                       // stage, pieces
     uint32_t ph = 0;
     bool ok = true;
-    while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+    while (ok && key_next(pl, w, w_end, job, pc)) {
       int r0, rn;
       const int nj = rows_of(r0, rn), b = kp_seq(pl, pc.job);
       // position of row r of tile t, -1 where there is none
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     uint32_t kph = 0;
     uint32_t cs = 0, cv = 0;                  // scores and P V products issued, parities
     bool ok = true;
-    while (ok && key_next(pl, a.Hkv, w, w_end, job, pc)) {
+    while (ok && key_next(pl, w, w_end, job, pc)) {
       int r0, rn;
       const bool mine = j < rows_of(r0, rn);
       const int nt = pc.t1 - pc.t0;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
         *abort_flag = 1;
       }
     };
-    while (key_next(pl, a.Hkv, w, w_end, job, pc)) {
+    while (key_next(pl, w, w_end, job, pc)) {
       int r0, rn;
       if (rows_of(r0, rn) <= j) continue;
       const int b = kp_seq(pl, pc.job);

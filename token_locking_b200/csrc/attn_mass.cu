@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
   int job = kp_job_at(pl, pl.wbase, w, lane);
   KeyPiece pc;
-  while (key_next(pl, 1, w, w_end, job, pc)) {
+  while (key_next(pl, w, w_end, job, pc)) {
     const int b = pc.job;
     const int i0 = pc.unit * MS_T, nv = min(MS_T, pl.kl[b] - i0);
     const int qn = pl.q0[b + 1] - pl.q0[b], nqt = kp_tiles(qn, QR);

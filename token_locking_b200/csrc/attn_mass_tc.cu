@@ -46,10 +46,10 @@ template <int D> struct KmCfg {
   // buffer full, free; drain
   static constexpr int B_KF = 0, B_KE = 1, B_F = 2, B_E = 2 + NS, B_TILE = 2 + 2 * NS;
   static constexpr int B_DRAIN = B_TILE + 8, B_COUNT = B_DRAIN + 2;
-  static constexpr int PLAN_OFF = BAR_OFF + 512;
+  static constexpr int PLAN_OFF = BAR_OFF + 256;
   static constexpr int CH = D / 8, RPI = 32 / CH;       // row copies: see the attention kernel
   static constexpr int NI = KM_KEYS / RPI / 2;          // instructions of each of two warps
-  static_assert(8 * B_COUNT + 8 <= 512 && sizeof(KeyPlan) <= TAIL - 512, "barriers and plan");
+  static_assert(8 * B_COUNT + 8 <= 256 && sizeof(KeyPlan) <= TAIL - 256, "barriers and plan");
   static_assert(SMEM <= 232448, "shared memory");
 };
 }  // namespace
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
     const uint32_t sw0 = ((ch ^ (pw * C::RPI + g0)) & 7) << 4, sw1 = sw0 ^ (4 << 4);
     int nk = 0;                               // K tiles copied
     int used = 0;                             // Q stages filled
-    while (ok && key_next(pl, 1, w, w_end, job, pc)) {
+    while (ok && key_next(pl, w, w_end, job, pc)) {
       const int b = pc.job, i0 = pc.unit * KM_KEYS;
       const int nj = pl.kl[b] - i0 > 128 ? 2 : 1;
       const int q0 = pl.q0[b], qn = pl.q0[b + 1] - q0, nqt = kp_tiles(qn, QR);
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
     const uint64_t dq = smem_desc_sw128(sbase + C::Q_OFF);
     int nk = 0;
     uint32_t cs = 0;                          // products issued
-    while (ok && key_next(pl, 1, w, w_end, job, pc)) {
+    while (ok && key_next(pl, w, w_end, job, pc)) {
       const int b = pc.job;
       const bool mine = j == 0 || pl.kl[b] - pc.unit * KM_KEYS > 128;
       const int nqt = kp_tiles(pl.q0[b + 1] - pl.q0[b], QR);
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
     const float c2 = a.scale * KEY_LOG2E;
     const f32x2 cc = pack2(c2, c2);
     uint32_t cs = 0;
-    while (ok && key_next(pl, 1, w, w_end, job, pc)) {
+    while (ok && key_next(pl, w, w_end, job, pc)) {
       const int b = pc.job, i0 = pc.unit * KM_KEYS + j * 128 + quarter * 32 + lane;
       const bool mine = j == 0 || pl.kl[b] - pc.unit * KM_KEYS > 128;
       const int qn = pl.q0[b + 1] - pl.q0[b], nqt = kp_tiles(qn, QR);

@@ -24,8 +24,9 @@ struct KeyPlan {
   int kl[SL_MAX_BATCH];       // keys of each sequence's set, in [0, n_ctx]
   int wbase[KP_JOBS + 1];     // first virtual tile of each job; from [njobs] W
   int T[KP_JOBS];             // inner tiles of a unit of the job
+  int nu[KP_JOBS];            // units of the job per K/V head
   int ubase[KP_JOBS + 1];     // first unit of each job, counted over all; from [njobs] their number
-  int njobs, stacked, chunk, per, ov, empty;   // empty: some sequence has rows and no keys
+  int njobs, stacked, chunk, per, ov, heads, empty;   // empty: some sequence has rows and no keys
 };
 
 // One piece of a unit, as one CTA computes it.
@@ -116,6 +117,8 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
   const int xp = stacked ? nu_p * a.Hkv : 0, cp = xp * (tp + ov);
   pl.T[b0 + sh] = T0;
   pl.T[b1 + sh] = T1;
+  pl.nu[b0 + sh] = max(weight ? t0 : u0, 1);
+  pl.nu[b1 + sh] = max(weight ? t1 : u1, 1);
   const int total = cp + __reduce_add_sync(0xffffffffu, c0 + c1);
   int share = (total + n_ctas - 1) / n_ctas;
   // the same in units, and the longest of them
@@ -154,6 +157,7 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
   if (lane == 0) {
     if (stacked) {
       pl.T[0] = tp;
+      pl.nu[0] = max(nu_p, 1);
       pl.wbase[0] = pl.ubase[0] = 0;
     }
     pl.q0[64] = ve;
@@ -162,6 +166,7 @@ __device__ inline void key_plan_build(KeyPlan &pl, const KeyArgs &a, int uq, int
     pl.njobs = B + sh;
     pl.stacked = stacked;
     pl.ov = ov;
+    pl.heads = a.Hkv;
     pl.empty = empty;
     pl.chunk = share;
     pl.per = per;
@@ -202,10 +207,20 @@ __device__ __forceinline__ int kp_bound(const KeyPlan &pl, int c, int lane) {
   return pl.wbase[j] + (u - pl.ubase[j]) * (pl.T[j] + pl.ov);
 }
 
+// Units follow one another head by head, so that the row blocks of a head meet its
+// keys together (1 to 3 % of the time); of a joint prefix's job, block by block
+// (head by head took 3 % more at two blocks of 256 rows over 8192 keys).
+__device__ __forceinline__ void kp_unit_of(const KeyPlan &pl, int job, int u, int &unit, int &hk) {
+  const bool by_block = pl.stacked && job == 0;
+  const int d = by_block ? pl.heads : pl.nu[job], q = u / d, r = u - q * d;
+  unit = by_block ? q : r;
+  hk = by_block ? r : q;
+}
+
 // The piece of the unit at virtual tile w that ends at or before w_end; w moves
 // to its end.  False once nothing is left; pieces without inner tiles (a cut
 // inside the start-up share) are passed over.
-__device__ __forceinline__ bool key_next(const KeyPlan &pl, int heads, int &w, int w_end, int &job,
+__device__ __forceinline__ bool key_next(const KeyPlan &pl, int &w, int w_end, int &job,
                                          KeyPiece &p) {
   while (w < w_end) {
     while (w >= pl.wbase[job + 1]) ++job;
@@ -218,8 +233,7 @@ __device__ __forceinline__ bool key_next(const KeyPlan &pl, int heads, int &w, i
     }
     const int v1 = min(cu, v0 + (w_end - w));
     p.job = job;
-    p.unit = u / heads;
-    p.hk = u - p.unit * heads;
+    kp_unit_of(pl, job, u, p.unit, p.hk);
     p.T = T;
     p.t0 = max(0, v0 - pl.ov);
     p.t1 = v1 - pl.ov;
