@@ -36,9 +36,10 @@
 // which the products need 1470 (416 + 320 each, measured alone) and the
 // exponentials 1280; the rest is the softmax warps' way from one barrier to the
 // next.  Long calls run at 1.4 GHz (clocks over nanoseconds) under the power
-// limit: 4 x 256 rows of 32 heads over a prefix of 16384 take 342 us back to back
-// (829 TFLOP/s) and 300 us after a pause, and neither a third fewer instructions
-// nor shifting the two chains against each other changed that.  Short calls are
+// limit, where a third fewer instructions or a shift of the two chains against
+// each other changed nothing, but less memory traffic did: 4 x 256 rows of 32
+// heads over a shared prefix of 16384 take 297 us back to back (953 TFLOP/s) with
+// the prefix read from memory once, 341 us with four times.  Short calls are
 // bound by starting: 0.9 us for the plan, 2.5 us to the first scores.
 #include <string.h>
 
