@@ -52,9 +52,8 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
   const int lr = tid >> 2, lc = (tid & 3) * 4;      // row and first column this thread stages
   const float c2 = a.scale * KEY_LOG2E;
 
-  int w = kp_bound(pl, blockIdx.x, lane);
-  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
-  int job = kp_job_at(pl, pl.wbase, w, lane);
+  int w, w_end, job;
+  key_begin(pl, blockIdx.x, lane, w, w_end, job);
   KeyPiece pc;
   while (key_next(pl, w, w_end, job, pc)) {
     const int b = kp_seq(pl, pc.job);

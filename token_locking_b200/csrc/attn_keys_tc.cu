@@ -157,9 +157,8 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   const int tp = kp_tiles(a.prefix_len, BN);
 
   // every role walks the same pieces
-  int w = kp_bound(pl, blockIdx.x, lane);
-  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
-  int job = kp_job_at(pl, pl.wbase, w, lane);
+  int w, w_end, job;
+  key_begin(pl, blockIdx.x, lane, w, w_end, job);
   KeyPiece pc{};
   // first query row and query rows of a piece's unit; row tiles it fills
   auto rows_of = [&](int &r0, int &rn) {

@@ -42,9 +42,8 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
   if (blockIdx.x == 0) key_plan_publish(pl, a.plan, tid, MS_THREADS);
   pdl_trigger();
   const float c2 = a.scale * KEY_LOG2E;
-  int w = kp_bound(pl, blockIdx.x, lane);
-  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
-  int job = kp_job_at(pl, pl.wbase, w, lane);
+  int w, w_end, job;
+  key_begin(pl, blockIdx.x, lane, w, w_end, job);
   KeyPiece pc;
   while (key_next(pl, w, w_end, job, pc)) {
     const int b = pc.job;

@@ -117,9 +117,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
   const uint32_t tmem_base = *tmem_slot;
 
   // every role walks the same pieces, and in them the same (K/V head, block)s
-  int w = kp_bound(pl, blockIdx.x, lane);
-  const int w_end = kp_bound(pl, blockIdx.x + 1, lane);
-  int job = kp_job_at(pl, pl.wbase, w, lane);
+  int w, w_end, job;
+  key_begin(pl, blockIdx.x, lane, w, w_end, job);
   KeyPiece pc{};
   int st = 0;                                 // Q stage
   uint32_t ph = 0;

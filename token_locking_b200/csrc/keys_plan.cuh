@@ -33,7 +33,6 @@ struct KeyPlan {
 struct KeyPiece {
   int job, unit, hk;          // row (or key) block and K/V head of the unit
   int t0, t1, T;              // inner tiles [t0, t1) of T
-  int w_unit;                 // the unit's first virtual tile
 };
 
 __device__ __forceinline__ int kp_tiles(int n, int tile) { return (n + tile - 1) / tile; }
@@ -197,14 +196,21 @@ __device__ __forceinline__ int kp_job_at(const KeyPlan &pl, const int *base, int
   return min(n, pl.njobs - 1);
 }
 
-// The first virtual tile of CTA c's share.
-__device__ __forceinline__ int kp_bound(const KeyPlan &pl, int c, int lane) {
+// CTA c's share: virtual tiles [w, w_end), or where shares are whole units, units
+// w, w + n_ctas, ... below w_end, so that the CTAs work on neighbouring units at a
+// time and a head's keys come from memory once (a run of neighbouring units per
+// CTA read 714 MB for 168 at 4 x 2048 rows over 1536 keys, 298 us instead of 252).
+__device__ __forceinline__ void key_begin(const KeyPlan &pl, int c, int lane, int &w, int &w_end,
+                                          int &job) {
   const int W = pl.wbase[pl.njobs];
-  if (!pl.per) return (int)min((long long)c * pl.chunk, (long long)W);
-  const int u = (int)min((long long)c * pl.per, (long long)pl.ubase[pl.njobs]);
-  if (u >= pl.ubase[pl.njobs]) return W;
-  const int j = kp_job_at(pl, pl.ubase, u, lane);
-  return pl.wbase[j] + (u - pl.ubase[j]) * (pl.T[j] + pl.ov);
+  if (pl.per) {
+    w = c;
+    w_end = pl.ubase[pl.njobs];
+  } else {
+    w = (int)min((long long)c * pl.chunk, (long long)W);
+    w_end = (int)min((long long)(c + 1) * pl.chunk, (long long)W);
+  }
+  job = kp_job_at(pl, pl.per ? pl.ubase : pl.wbase, w, lane);
 }
 
 // Units follow one another head by head, so that the row blocks of a head meet its
@@ -217,11 +223,21 @@ __device__ __forceinline__ void kp_unit_of(const KeyPlan &pl, int job, int u, in
   hk = by_block ? r : q;
 }
 
-// The piece of the unit at virtual tile w that ends at or before w_end; w moves
-// to its end.  False once nothing is left; pieces without inner tiles (a cut
-// inside the start-up share) are passed over.
+// The piece of the unit at virtual tile w that ends at or before w_end (or the
+// whole unit w); w moves behind it.  False once nothing is left; pieces without
+// inner tiles (a cut inside the start-up share) are passed over.
 __device__ __forceinline__ bool key_next(const KeyPlan &pl, int &w, int w_end, int &job,
                                          KeyPiece &p) {
+  if (pl.per) {
+    if (w >= w_end) return false;
+    while (w >= pl.ubase[job + 1]) ++job;
+    p.job = job;
+    kp_unit_of(pl, job, w - pl.ubase[job], p.unit, p.hk);
+    p.T = p.t1 = pl.T[job];
+    p.t0 = 0;
+    w += gridDim.x;
+    return true;
+  }
   while (w < w_end) {
     while (w >= pl.wbase[job + 1]) ++job;
     const int T = pl.T[job], cu = T + pl.ov;
@@ -237,7 +253,6 @@ __device__ __forceinline__ bool key_next(const KeyPlan &pl, int &w, int w_end, i
     p.T = T;
     p.t0 = max(0, v0 - pl.ov);
     p.t1 = v1 - pl.ov;
-    p.w_unit = w - v0;
     w += v1 - v0;
     if (p.t1 > p.t0) return true;
   }
