@@ -2,8 +2,8 @@
 // the 5th-generation tensor cores, for bf16 heads of 64 and 128.
 //
 // A unit is two tiles of 128 packed rows (query row, head of the group) of one
-// K/V head against a list of tiles of BN keys; a CTA takes an equal share of
-// all units' tiles (keys_plan.cuh) and runs through its pieces without a break:
+// K/V head against a list of tiles of BN keys; a CTA takes whole units or an equal
+// share of all their tiles (keys_plan.cuh) and runs through them without a break:
 //   warps 0,3    producers.  Warp 0 copies Q by TMA in boxes [QR query rows]
 //                [G heads][64], so that packed rows land in order whatever G,
 //                and every full tile of the prefix or of an unlisted cache.
@@ -38,8 +38,8 @@
 // next.  Long calls run at 1.4 GHz (clocks over nanoseconds) under the power
 // limit, where a third fewer instructions or a shift of the two chains against
 // each other changed nothing, but less memory traffic did: 4 x 256 rows of 32
-// heads over a shared prefix of 16384 take 297 us back to back (953 TFLOP/s) with
-// the prefix read from memory once, 341 us with four times.  Short calls are
+// heads over a shared prefix of 16384 take 285 to 317 us back to back (cards differ)
+// with the prefix read from memory once, 341 us with four times.  Short calls are
 // bound by starting: 0.9 us for the plan, 2.5 us to the first scores.
 #include <string.h>
 
