@@ -501,9 +501,9 @@ sl_status sl_key_attention(sl_key_attn *a, int rows, const void *d_q, int64_t ld
  * sl_key_attention left for these rows (prefix included): the attention weight
  * each cached entry received, to be accumulated over layers and steps.  mass and
  * mass_prev: [batch][n_ctx] fp32, may be the same; decay = 0 does not read
- * mass_prev (may be NULL).  Rows with lse = -inf weigh nothing.  The same call gives
- * the same bits, unless a list names a position more than once (its weights are
- * then added in no fixed order). */
+ * mass_prev (may be NULL).  Rows with lse = -inf weigh nothing, whatever their q
+ * holds.  The same call gives the same bits, unless a list names a position more
+ * than once (its weights are then added in no fixed order). */
 sl_status sl_key_mass(sl_key_attn *a, int rows, const void *d_q, int64_t ld_q, const void *d_k,
                       int64_t ld_kv, const sl_key_set *set, const float *d_lse, float decay,
                       const float *d_mass_prev, float *d_mass, void *stream);

@@ -73,12 +73,9 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
               lr < rn ? load4(src + c) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       if (tid < MS_T) {
-        // rows that are not there, or saw no key, weigh nothing
-        float L = INFINITY;
-        if (tid < rn) {
-          L = a.lse[(size_t)(r0 + tid / a.G) * a.H + hk * a.G + tid % a.G] * KEY_LOG2E;
-          if (L == -INFINITY) L = INFINITY;
-        }
+        // -inf: rows that are not there, or saw no key, weigh nothing
+        float L = -INFINITY;
+        if (tid < rn) L = a.lse[(size_t)(r0 + tid / a.G) * a.H + hk * a.G + tid % a.G] * KEY_LOG2E;
         sL[tid] = L;
       }
       __syncthreads();
@@ -105,8 +102,8 @@ __global__ void __launch_bounds__(MS_THREADS) key_mass_simt_kernel(const KeyArgs
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float L = sL[4 * ty + i];
-          // a select, not a product: the score may be NaN where L is +inf
-          acc[j] += L == INFINITY ? 0.f : exp2f(fmaf(s[i][j], c2, -L));
+          // a select: the score may be anything where L is -inf
+          acc[j] += L == -INFINITY ? 0.f : exp2f(fmaf(s[i][j], c2, -L));
         }
     }
     // the key's sum over the 16 row groups

@@ -7,8 +7,9 @@
 // (query row, head of the group) of every K/V head:
 //   warp 0       TMA producer: the two K tiles once per K/V head, the Q blocks
 //                (boxes [QR query rows][G heads][64]) through a ring
-//   warp 3       -lse log2(e) of a block's rows into the ring; with warp 0, rows
-//                of listed keys (16-byte asynchronous copies)
+//   warp 3       -lse log2(e) of a block's rows into the ring, and a mark where
+//                some of them weigh nothing; with warp 0, rows of listed keys
+//                (16-byte asynchronous copies)
 //   warps 1,2    one lane each issues the products of key tile j, into one of
 //                two score buffers
 //   warps 4..19  two warpgroups per key tile: a thread sums
@@ -34,12 +35,20 @@ namespace {
 constexpr int KM_THREADS = 128 + 4 * 128;
 constexpr int KM_KEYS = 256;                  // keys of a unit
 constexpr int KM_HALF = 64;                   // rows of a block that a thread sums
+// In place of the first -lse log2(e) of a half block: some of its rows weigh
+// nothing.  (A NaN; a half block that begins with this very one takes the marked
+// path too.  The bits read for every half block instead: 1.4 % of the long call's
+// time, in the queue that the exponentials wait in; the mark 0.5 %.)
+constexpr uint32_t KM_MARK = 0x7fc0a5a5u;
 
 template <int D> struct KmCfg {
   static constexpr int NB = D / 64;                     // 128-byte boxes of a row
   static constexpr int BOX = 128 * 128, TILE = NB * BOX;
   static constexpr int TAIL = 2048;
-  static constexpr int K_OFF = 0, Q_OFF = 2 * TILE, STAGE = TILE + 1024;   // + lse, aligned
+  // a stage: Q block, lse of its 128 rows with marks, the same without, a bit for
+  // each row that weighs nothing; aligned
+  static constexpr int K_OFF = 0, Q_OFF = 2 * TILE, LSE = TILE, PLAIN = 512, OUT = TILE + 1024;
+  static constexpr int STAGE = TILE + 2048;
   static constexpr int NS = D == 128 ? 4 : 6;           // Q blocks in flight
   static constexpr int BAR_OFF = Q_OFF + NS * STAGE, SMEM = BAR_OFF + TAIL + 1024;
   // barriers: K full, K free; per Q stage full, free; per key tile and score
@@ -143,19 +152,16 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
       const int nj = pl.kl[b] - i0 > 128 ? 2 : 1;
       const int q0 = pl.q0[b], qn = pl.q0[b + 1] - q0, nqt = kp_tiles(qn, QR);
       int hk = pc.t0 / nqt, blk = pc.t0 - hk * nqt;
-      // -lse log2(e) of this lane's four rows of a block (warp 3); rows that are
-      // not there, or saw no key, weigh nothing
+      // -lse log2(e) of this lane's four rows of a block (warp 3); +inf: rows that
+      // are not there, or saw no key, weigh nothing
       float nl[4];
       auto lse_of = [&](int h, int bk) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = 32 * e + lane, rq = r / a.G;
-          float x = -INFINITY;
-          if (rq < QR && bk * QR + rq < qn) {
-            x = -a.lse[(size_t)(q0 + bk * QR + rq) * a.H + h * a.G + r - rq * a.G] * KEY_LOG2E;
-            if (x == INFINITY) x = -INFINITY;
-          }
-          nl[e] = x;
+          nl[e] = rq < QR && bk * QR + rq < qn
+                      ? -a.lse[(size_t)(q0 + bk * QR + rq) * a.H + h * a.G + r - rq * a.G] * KEY_LOG2E
+                      : INFINITY;
         }
       };
       if (pw == 1) lse_of(hk, blk);
@@ -205,9 +211,24 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
                           bar(C::B_F + st));
           }
         } else {
-          float *dst = reinterpret_cast<float *>(smem + C::Q_OFF + st * C::STAGE + C::TILE);
+          uint8_t *dst = smem + C::Q_OFF + st * C::STAGE;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[32 * e + lane] = nl[e];
+          for (int e = 0; e < 4; e += 2) {
+            const uint32_t lo = __ballot_sync(0xffffffffu, nl[e] == INFINITY);
+            const uint32_t hi = __ballot_sync(0xffffffffu, nl[e + 1] == INFINITY);
+            const float x = nl[e] == INFINITY ? 0.f : nl[e];
+            const float y = nl[e + 1] == INFINITY ? 0.f : nl[e + 1];
+            const bool mark =
+                __any_sync(0xffffffffu, (lo | hi) != 0 || __float_as_uint(x) == KM_MARK);
+            float *to = reinterpret_cast<float *>(dst + C::LSE) + 32 * e + lane;
+            to[0] = mark && lane == 0 ? __uint_as_float(KM_MARK) : x;
+            to[32] = y;
+            if (mark) {
+              to[C::PLAIN / 4] = x;
+              to[C::PLAIN / 4 + 32] = y;
+              if (lane == 0) reinterpret_cast<uint2 *>(dst + C::OUT)[e / 2] = make_uint2(lo, hi);
+            }
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::B_F + st));
         }
@@ -308,10 +329,6 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
     while (ok && key_next(pl, w, w_end, job, pc)) {
       const int b = pc.job, i0 = pc.unit * KM_KEYS + j * 128 + quarter * 32 + lane;
       const bool mine = j == 0 || pl.kl[b] - pc.unit * KM_KEYS > 128;
-      const int qn = pl.q0[b + 1] - pl.q0[b], nqt = kp_tiles(qn, QR);
-      const int n_last = (qn - (nqt - 1) * QR) * a.G;    // packed rows of the last block
-      const int n_full = QR * a.G;
-      int blk = pc.t0 % nqt;
       f32x2 sum[2] = {0ull, 0ull};
       for (int t = pc.t0; t < pc.t1; ++t) {
         ok = key_wait(bar(C::B_F + st), ph, abort_flag, lim);
@@ -321,9 +338,17 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
           ok = key_wait(tfull(j, u), (cs >> 1) & 1u, abort_flag, lim);
           if (!ok) break;
           tc_fence_after();
-          const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(
-              smem + C::Q_OFF + st * C::STAGE + C::TILE) + half * (KM_HALF / 4);
-          const int nv = (blk + 1 == nqt ? n_last : n_full) - half * KM_HALF;
+          const uint8_t *stage = smem + C::Q_OFF + st * C::STAGE;
+          const ulonglong2 *nl =
+              reinterpret_cast<const ulonglong2 *>(stage + C::LSE) + half * (KM_HALF / 4);
+          ulonglong2 x = nl[0];
+          uint2 out = make_uint2(0u, 0u);
+          if ((uint32_t)x.x == KM_MARK) {
+            key_cold();
+            out = reinterpret_cast<const uint2 *>(stage + C::OUT)[half];
+            nl += C::PLAIN / 16;
+            x = nl[0];
+          }
 #pragma unroll
           for (int c = 0; c < KM_HALF; c += 32) {
             float s[32];
@@ -333,14 +358,15 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
               __syncwarp();
               if (lane == 0) mbar_arrive(tfree(j, u));
             }
-            if (nv < KM_HALF) {               // rows that are not there may hold anything
+            // rows that weigh nothing may hold anything, NaN among it
+            if (const uint32_t bits = c == 0 ? out.x : out.y) {
               key_cold();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[i] = c + i < nv ? s[i] : -INFINITY;
+              for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1 ? -INFINITY : s[i];
             }
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const ulonglong2 x = nl[(c + i) / 4];
+              if (c + i > 0) x = nl[(c + i) / 4];
               float p[4];
               unpack2(fma2(pack2(s[i], s[i + 1]), cc, x.x), p[0], p[1]);
               unpack2(fma2(pack2(s[i + 2], s[i + 3]), cc, x.y), p[2], p[3]);
@@ -354,7 +380,6 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::B_E + st));
-        if (++blk == nqt) blk = 0;
         next_stage();
       }
       if (ok && mine && i0 < pl.kl[b]) {
