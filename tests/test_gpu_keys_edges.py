@@ -56,3 +56,24 @@ def test_rows_with_lse_of_plus_infinity_follow_the_formula(cuda_dev, dtype, dh):
     ka.mass(c.q, c.k, lse, mass, c.seq_off, key_len=c.key_len)
     assert torch.isnan(mass[1, :60]).all() and (mass[1, 60:] == 0).all()
     assert _within(mass[:1], want[:1], bound[:1])
+
+
+@pytest.mark.parametrize("keys,prefix", [(90, 0), (3000, 0), (70, 500)])
+@pytest.mark.parametrize("dtype,dh", KERNELS)
+def test_rows_of_minus_infinity_give_zero_whatever_v_holds(cuda_dev, dtype, dh, keys, prefix):
+    """A row whose scores are all -inf gets o = 0 and lse = -inf, also where v is
+    infinite or NaN, in whole units, in cut ones and over a joint prefix."""
+    c = Case(cuda_dev, dtype, [20, 5], [keys, 33], keys, 2, 1, dh, prefix, seed=53)
+    c.q.copy_((c.q.abs() + 0.1).to(c.dt))                # positive: the score's sign is the key's
+    c.k[:keys] = -math.inf
+    c.v[:keys:3], c.v[1:keys:3] = math.inf, float("nan")
+    if prefix:                                           # then the other sequence sees no key either
+        c.kp.fill_(-math.inf)
+        c.vp.fill_(math.inf)
+        c.k[keys:] = -math.inf
+    ka = c.key_attention()
+    o, lse = c.outputs()
+    c.attend(ka, o, lse)
+    n = 25 if prefix else 20
+    assert (o[:n] == 0).all() and (lse[:n] == -math.inf).all()
+    assert torch.isfinite(o[20:]).all() and torch.isfinite(lse[n:]).all()

@@ -188,13 +188,12 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
       if (r >= rn) continue;
       const int row = r0 + r / a.G, h = pc.hk * a.G + r % a.G;
       if (whole && !pl.stacked) {
-        const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+        const float inv = key_inv(l[i]);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           if (4 * tx + 64 * c < D)
             store4((T *)a.o + row * a.ld_o + h * D + 4 * tx + 64 * c,
-                   make_float4(acc[i][c].x * inv, acc[i][c].y * inv, acc[i][c].z * inv,
-                               acc[i][c].w * inv));
+                   key_mean(acc[i][c], l[i], inv));
         if (a.lse && tx == 0)
           a.lse[(size_t)row * a.H + h] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * KEY_LN2;
         continue;
@@ -242,10 +241,8 @@ __device__ __forceinline__ void join_rec(JoinAcc &x, float2 ml, float4 u) {
 template <typename T>
 __device__ __forceinline__ void join_store(const KeyArgs &a, const JoinAcc &x, int row, int h,
                                            int lane) {
-  const float inv = x.l > 0.f ? 1.f / x.l : (x.l == 0.f ? 0.f : x.l);
   if (4 * lane < a.D)
-    store4((T *)a.o + row * a.ld_o + h * a.D + 4 * lane,
-           make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+    store4((T *)a.o + row * a.ld_o + h * a.D + 4 * lane, key_mean(x.o, x.l, key_inv(x.l)));
   if (a.lse && lane == 0)
     a.lse[(size_t)row * a.H + h] = x.l == 0.f ? -INFINITY : (x.m + log2f(x.l)) * KEY_LN2;
 }

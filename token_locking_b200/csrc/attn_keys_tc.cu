@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       const bool whole = pc.t0 == 0 && pc.t1 == pc.T;
       float o[32];
       if (whole && !pl.stacked) {
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const float inv = key_inv(l);
         bf16 *orow = (bf16 *)a.o + row * a.ld_o + h * D + half * (D / 2);
 #pragma unroll 1
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
           if (live) {
             uint32_t u[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) u[c] = kc_pack(o[2 * c] * inv, o[2 * c + 1] * inv);
+            for (int c = 0; c < 16; ++c)
+              u[c] = l == 0.f ? 0u : kc_pack(o[2 * c] * inv, o[2 * c + 1] * inv);
             if (o32) {
               st_global_v8(orow + c0, u);
               st_global_v8(orow + c0 + 16, u + 8);

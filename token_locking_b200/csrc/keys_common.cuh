@@ -25,6 +25,14 @@ __device__ __forceinline__ void store4(bf16 *p, float4 v) {
   *reinterpret_cast<uint2 *>(p) = u;
 }
 
+// 1 / l for a row's sum of weights l: a NaN stays one.
+__device__ __forceinline__ float key_inv(float l) { return l > 0.f ? 1.f / l : l; }
+// o / l; 0 for a row without weight, whose o may be 0 times an infinite v.
+__device__ __forceinline__ float4 key_mean(float4 o, float l, float inv) {
+  if (l == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+  return make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
 // Position of entry i of sequence b's key set; -1 for a list entry outside
 // [0, n_ctx), which stands for a key and value of zeros and is reported.
 __device__ __forceinline__ int key_pos(const KeyArgs &a, int b, int i) {
