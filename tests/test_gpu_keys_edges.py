@@ -6,6 +6,8 @@ import pytest
 import torch
 
 from keys_util import Case, ref_mass
+from token_locking_b200 import _abi as A
+from token_locking_b200 import runtime as rt
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +79,18 @@ def test_rows_of_minus_infinity_give_zero_whatever_v_holds(cuda_dev, dtype, dh, 
     n = 25 if prefix else 20
     assert (o[:n] == 0).all() and (lse[:n] == -math.inf).all()
     assert torch.isfinite(o[20:]).all() and torch.isfinite(lse[n:]).all()
+
+
+def test_budgets_beyond_32_bits(cuda_dev):
+    """Any budget above the cache keeps everything, any negative one is refused."""
+    m = torch.rand((2, 50), device=cuda_dev)
+    for budget in (50, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 7, 10 ** 15):
+        keys = torch.full((2, 50), -9, dtype=torch.int32, device=cuda_dev)
+        n = torch.full((2,), -9, dtype=torch.int32, device=cuda_dev)
+        rt.kv_evict(m, budget, keys, n)
+        assert n.tolist() == [50, 50]
+        assert torch.equal(keys.cpu(), torch.arange(50, dtype=torch.int32).repeat(2, 1))
+    for budget in (-1, -(2 ** 31) - 1, -(2 ** 32), -(2 ** 32) + 7):
+        with pytest.raises(A.SureLockError) as e:
+            rt.kv_evict(m, budget, keys, n)
+        assert e.value.status == A.SL_ERR_INVALID

@@ -581,7 +581,8 @@ def kv_evict(mass: torch.Tensor, budget: int, keys: torch.Tensor, key_len: torch
         raise ValueError("mass must be a CUDA tensor [batch, n_ctx]")
     B, N = shape = tuple(mass.shape)
     dev, u8 = mass.get_device(), torch.uint8
-    _call_on(dev, A.lib().sl_kv_evict, "sl_kv_evict", stream, B, N, int(budget),
+    room = max(min(int(budget), N), -1)          # as a C int: all above N are the same
+    _call_on(dev, A.lib().sl_kv_evict, "sl_kv_evict", stream, B, N, room,
              _dense_ptr(mass, "mass", dev, torch.float32, shape),
              _dense_ptr(protect, "protect", dev, u8, shape),
              _dense_ptr(present, "present", dev, u8, shape),
