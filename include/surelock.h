@@ -454,8 +454,8 @@ void sl_sampler_destroy(sl_sampler *s);
 typedef struct sl_key_attn sl_key_attn;
 typedef struct sl_key_attn_config {
   int dtype;             /* sl_dtype of q, k, v and o */
-  int batch, n_ctx;      /* sequences (1..SL_MAX_BATCH); cache rows of each */
-  int max_rows;          /* most query rows of a call */
+  int batch, n_ctx;      /* sequences (1..SL_MAX_BATCH); cache rows of each (all: 2^31 - 2^16) */
+  int max_rows;          /* most query rows of a call (up to 2^31 - 2^16) */
   int n_heads;           /* query heads, a multiple of n_kv_heads (64 times at most) */
   int n_kv_heads;        /* head h reads K/V head h * n_kv_heads / n_heads */
   int head_dim;          /* up to 128, 16-byte multiples (bf16 64 and 128: tensor cores) */

@@ -35,6 +35,8 @@ sl_status fill_args(const sl_key_attn *a, const char *fn, int rows, const void *
                     int prefix_len, KeyArgs *x) {
   if (!a) return fail(SL_ERR_INVALID, "%s: null object", fn);
   const sl_key_attn_config &c = a->cfg;
+  if (prefix_len < 0 || prefix_len > KEY_MAX_ROWS)
+    return fail(SL_ERR_INVALID, "%s: prefix_len %d outside [0, 2^31 - 2^16]", fn, prefix_len);
   int dev = -1;
   SL_CUDA(cudaGetDevice(&dev));
   if (dev != a->device)
@@ -50,7 +52,6 @@ sl_status fill_args(const sl_key_attn *a, const char *fn, int rows, const void *
   if (!rows_ok(d_k, ld_kv, c.n_kv_heads * c.head_dim, es))
     return fail(SL_ERR_INVALID, "%s: k/v need 16-byte aligned rows of at least %d columns", fn,
                 c.n_kv_heads * c.head_dim);
-  if (prefix_len < 0) return fail(SL_ERR_INVALID, "%s: prefix_len %d < 0", fn, prefix_len);
   // the work plan counts (row block, head, key tile) triples in 32 bits
   const double tiles = (double)(prefix_len + (double)c.n_ctx) / 64.0 + 4;
   const double blocks = c.n_kv_heads * ((double)rows * a->group / 32.0 + 2.0 * c.batch);
@@ -89,10 +90,12 @@ extern "C" sl_status sl_key_attn_create(const sl_key_attn_config *cfg, sl_key_at
   if (cfg->dtype != SL_F32 && cfg->dtype != SL_BF16)
     return fail(SL_ERR_INVALID, "sl_key_attn_create: dtype %d", cfg->dtype);
   if (cfg->batch < 1 || cfg->batch > SL_MAX_BATCH || cfg->n_ctx < 1 ||
-      (long long)cfg->batch * cfg->n_ctx > INT_MAX)
+      (long long)cfg->batch * cfg->n_ctx > KEY_MAX_ROWS)
     return fail(SL_ERR_INVALID, "sl_key_attn_create: batch in [1, %d], n_ctx > 0 and batch * n_ctx "
-                "below 2^31 required", SL_MAX_BATCH);
-  if (cfg->max_rows < 1) return fail(SL_ERR_INVALID, "sl_key_attn_create: max_rows < 1");
+                "up to 2^31 - 2^16 required", SL_MAX_BATCH);
+  if (cfg->max_rows < 1 || cfg->max_rows > KEY_MAX_ROWS)
+    return fail(SL_ERR_INVALID, "sl_key_attn_create: max_rows %d outside [1, 2^31 - 2^16]",
+                cfg->max_rows);
   if (cfg->n_heads < 1 || cfg->n_kv_heads < 1 || cfg->n_heads % cfg->n_kv_heads != 0)
     return fail(SL_ERR_INVALID, "sl_key_attn_create: n_kv_heads %d does not divide n_heads %d",
                 cfg->n_kv_heads, cfg->n_heads);

@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 
 #include <utility>
@@ -231,6 +232,10 @@ cudaError_t launch_gemm_tc(const TcGemmArgs &a, int num_sms, int *err, cudaStrea
 // receives (see keys_plan.cuh for how the work is shared out).
 constexpr int KP_JOIN_NUM = 1, KP_JOIN_DEN = 16;   // joining one packed row, in tile times
 constexpr int KEY_PLAN_WORDS = 512;
+// Most query rows, cache rows (batch * n_ctx) and prefix rows of a call: they are
+// counted in 32 bits, and tiles (256 rows) and grid strides (1024 blocks of 32
+// entries) run past the last one.
+constexpr int KEY_MAX_ROWS = INT_MAX - (1 << 16) + 1;   // 2^31 - 2^16
 struct KeyArgs {
   int dtype, batch, n_ctx, M, H, Hkv, G, D;   // G = H / Hkv query heads per K/V head
   int prefix_len;

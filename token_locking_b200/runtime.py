@@ -533,6 +533,8 @@ class KeyAttention:
         lp = n_prefix = 0
         if k_prefix is not None and k_prefix.shape[0] > 0:
             n_prefix = k_prefix.shape[0]
+            if n_prefix >= 1 << 31:              # would not fit a C int
+                raise ValueError(f"k_prefix has {n_prefix} rows")
             pkp, lp = _rows_ptr(k_prefix, "k_prefix", dev, dt, hkd)
             pvp, lvp = _rows_ptr(v_prefix, "v_prefix", dev, dt, hkd, n_prefix)
             if lp != lvp:
