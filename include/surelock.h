@@ -551,12 +551,13 @@ sl_status sl_device_check(int clear);
  * and returns, and the context stays usable.
  *   sl_debug_set_wait_limit: every later tensor-core GEMM and attention launch
  *     (sl_step, sl_step_stats, sl_layer_forward, sl_attention, sl_gemm_bf16,
- *     autotuning) gives up a barrier wait after `ns` nanoseconds instead of
+ *     sl_key_attention, sl_key_mass, autotuning) gives up a barrier wait after `ns` nanoseconds instead of
  *     the default 2 s; 0 restores the default.
  *     SL_ERR_INVALID outside [1 ms, 2 s].  Process-wide.
- *   sl_debug_inject_lost_load: the next tensor-core GEMM launch on the 1-SM
- *     kernels has its first CTA leave out the operand copies of its first
- *     pipeline stage, so the MMA warp's wait for them runs out (one-shot). */
+ *   sl_debug_inject_lost_load: the next tensor-core launch of a GEMM on the 1-SM
+ *     kernels, of sl_key_attention or of sl_key_mass has its first CTA leave out
+ *     the operand copies of its first pipeline stage (the key-set operators: of its
+ *     first key tile), so the MMA warp's wait for them runs out (one-shot). */
 sl_status sl_debug_set_wait_limit(unsigned long long ns);
 sl_status sl_debug_inject_lost_load(void);
 

@@ -1,8 +1,10 @@
 // Host-only checks of the key-set operators (no GPU needed): sizes whose tile
-// arithmetic would pass 32 bits are refused before anything is launched.  It
+// arithmetic would pass 32 bits are refused before anything is launched, and a
+// kernel that gives up waits for the last fill of every stage of its ring.  It
 // includes the host side's source so that it sees objects as the library makes
 // them.
 #include "api_keys.cu"
+#include "keys_tc.cuh"
 
 #include <cstdio>
 
@@ -51,8 +53,28 @@ static void check_sizes() {
   CHECK(sl_key_attn_create(&c, &out) == SL_ERR_INVALID && !out, "64 x 2^25");
 }
 
+// A barrier that has completed n phases lets a waiter for parity p pass if the
+// phase under way has the other one.
+static bool passes(int n, uint32_t p) { return ((uint32_t)n & 1u) != p; }
+
+static void check_rings() {
+  for (int stages = 1; stages <= 9; ++stages)
+    for (int fills = 0; fills <= 4 * stages + 1; ++fills) {
+      const int st = fills % stages;
+      const uint32_t ph = (uint32_t)(fills / stages) & 1u;
+      for (int s = 0; s < stages; ++s) {
+        const int own = fills / stages + (s < st);   // fills of this stage
+        const uint32_t p = key_ring_parity(s, st, ph);
+        CHECK(passes(own, p), "stage %d of %d after %d fills, all landed", s, stages, fills);
+        CHECK(own == 0 || !passes(own - 1, p), "stage %d of %d after %d fills, one in flight", s,
+              stages, fills);
+      }
+    }
+}
+
 int main() {
   check_sizes();
+  check_rings();
   printf("%ld checks, %d failures\n", g_checked, g_fail);
   return g_fail != 0;
 }

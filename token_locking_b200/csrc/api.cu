@@ -789,11 +789,12 @@ static sl_status layer_f32(sl_model *m, sl_kv_cache *c, sl_active *a, int l, flo
   return SL_OK;
 }
 
-// Failure-detection test hooks (sl_debug_*): the wait limit of later GEMM
+// Failure-detection test hooks (sl_debug_*): the wait limit of later tensor-core
 // launches, and a one-shot lost operand copy in the next one.
 static std::atomic<unsigned long long> g_wait_limit_ns{0};
 unsigned long long sl::wait_limit_ns() { return g_wait_limit_ns.load(std::memory_order_relaxed); }
 static std::atomic<int> g_lost_load{0};
+int sl::take_lost_load() { return g_lost_load.exchange(0, std::memory_order_relaxed); }
 
 // Split-K tile fix-up in the GEMM epilogue instead of a finalize kernel
 // (SL_GEMM_FIXUP=0 turns it off; read once).
@@ -808,7 +809,7 @@ static bool gemm_fixup_enabled() {
 
 static cudaError_t launch_gemm_hooked(TcGemmArgs g, int num_sms, int *err, cudaStream_t s) {
   g.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  g.lost_load = g_lost_load.exchange(0, std::memory_order_relaxed);
+  g.lost_load = take_lost_load();
   return launch_gemm_tc(g, num_sms, err, s);
 }
 

@@ -182,6 +182,7 @@ extern "C" sl_status sl_key_attention(sl_key_attn *a, int rows, const void *d_q,
   x.ld_o = ld_o;
   x.lse = d_lse;
   x.n_ctas = a->attn_ctas;
+  x.lost = key_attn_tc_takes(c.dtype, c.head_dim) ? take_lost_load() : 0;
   SL_CUDA(launch_key_attn(x, (cudaStream_t)stream));
   return SL_OK;
 }
@@ -203,6 +204,7 @@ extern "C" sl_status sl_key_mass(sl_key_attn *a, int rows, const void *d_q, int6
   x.mass_prev = d_mass_prev;
   x.mass = d_mass;
   x.n_ctas = a->mass_ctas;
+  x.lost = rows > 0 && key_attn_tc_takes(x.dtype, x.D) ? take_lost_load() : 0;
   SL_CUDA(launch_key_mass(x, (cudaStream_t)stream));
   return SL_OK;
 }

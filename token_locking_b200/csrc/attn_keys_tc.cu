@@ -82,7 +82,7 @@ template <int D, int BN> struct KcCfg {
   static constexpr uint32_t L_COL = X_COL + 4;          // and row sums
   static_assert(O_COL + 2 * D <= 512 && L_COL + 2 <= T_COLS, "TMEM columns");
   static constexpr int HB = BN / 2;                     // keys of a softmax warpgroup
-  static_assert(8 * B_COUNT + 8 <= 256 && sizeof(KeyPlan) <= TAIL - 256, "barriers and plan");
+  static_assert(8 * B_COUNT + 20 <= 256 && sizeof(KeyPlan) <= TAIL - 256, "barriers and plan");
   static_assert(BN % (2 * RPI) == 0 && NI * RPI <= 64, "two rows a lane of a warp's share");
   static_assert(LAG < NP, "row copies in flight");
   static_assert(SMEM <= 232448 && BN % 16 == 0, "shared memory, key tile");
@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   auto tbar = [&](int j, int k) { return bar0 + 8u * (uint32_t)(C::B_TILE + 4 * j + k); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::B_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  KeyFills *fills = reinterpret_cast<KeyFills *>(tmem_slot + 2);
   KeyPlan &pl = *reinterpret_cast<KeyPlan *>(smem + C::PLAN_OFF);
   const KeyArgs &a = p.a;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
     int st = 0, np = 0;                       // stage, pieces
     uint32_t ph = 0;
     bool ok = true;
+    bool lost = a.lost && blockIdx.x == 0 && pw == 0;   // test hook: the first tile is left out
     while (ok && key_next(pl, w, w_end, job, pc)) {
       int r0, rn;
       const int nj = rows_of(r0, rn), b = kp_seq(pl, pc.job);
@@ -209,7 +211,8 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       auto hand_over = [&]() {
         fence_proxy_async_smem();             // written by copies, read by the tensor cores
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_F + pst));
+        if (lane == 0 && !lost) mbar_arrive(bar(C::B_F + pst));
+        lost = false;
         pst = pst + 1 == C::NP ? 0 : pst + 1;
         --pend;
       };
@@ -247,7 +250,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
             hand_over();
           }
         } else {
-          if (lane == 0) {
+          if (lane == 0 && !lost) {
             if (pw == 0) {
               const int y = pre ? i0 : b * a.n_ctx + i0;
               mbar_expect_tx(bar(C::B_F + st), 2 * C::SLOT);
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
               mbar_arrive(bar(C::B_F + st));
             }
           }
+          lost = false;
           pst = st + 1 == C::NP ? 0 : st + 1;
         }
         if (++st == C::NP) {
@@ -281,15 +285,7 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
       atomicExch(a.err, DEV_TIMEOUT_PRODUCER);
       *abort_flag = 1;
     }
-    // Every copy lands before the CTA can exit: the issuing warps have waited for
-    // each stage, unless a wait ran out.  Then the stages' last fills are waited
-    // for here; one that not both producers handed over costs its share of the limit.
-    if (pw == 0 && lane == 0 && *abort_flag) {
-      volatile int never = 0;
-      if (np > 0) mbar_wait(bar(C::B_QF), (uint32_t)(np - 1) & 1u, &never, lim);
-      for (int s = 0; s < C::NP; ++s)
-        mbar_wait(bar(C::B_F + s), s <= st ? ph : ph ^ 1u, &never, lim / C::NP);
-    }
+    if (pw == 0 && lane == 0) *fills = KeyFills{st, (int)ph, np};
   } else if (warp < 3) {
     // ------------------------------------------------------------- MMA
     const int j = warp - 1;                   // row tile
@@ -532,6 +528,8 @@ __global__ void __launch_bounds__(KC_THREADS, 1) key_attn_tc_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // no role can raise the flag any more
+  if (threadIdx.x == 0 && *abort_flag) key_drain(*fills, bar(C::B_F), C::NP, bar(C::B_QF), lim);
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),

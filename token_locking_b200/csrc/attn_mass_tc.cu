@@ -58,7 +58,7 @@ template <int D> struct KmCfg {
   static constexpr int PLAN_OFF = BAR_OFF + 256;
   static constexpr int CH = D / 8, RPI = 32 / CH;       // row copies: see the attention kernel
   static constexpr int NI = KM_KEYS / RPI / 2;          // instructions of each of two warps
-  static_assert(8 * B_COUNT + 8 <= 256 && sizeof(KeyPlan) <= TAIL - 256, "barriers and plan");
+  static_assert(8 * B_COUNT + 20 <= 256 && sizeof(KeyPlan) <= TAIL - 256, "barriers and plan");
   static_assert(SMEM <= 232448, "shared memory");
 };
 }  // namespace
@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
   auto tfree = [&](int j, int u) { return bar0 + 8u * (uint32_t)(C::B_TILE + 4 * j + 2 + u); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::BAR_OFF + 8 * C::B_COUNT);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  KeyFills *fills = reinterpret_cast<KeyFills *>(tmem_slot + 2);
   KeyPlan &pl = *reinterpret_cast<KeyPlan *>(smem + C::PLAN_OFF);
   const KeyArgs &a = p.a;
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -146,7 +147,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
     const uint32_t off = (ch >> 3) * C::BOX + (pw * C::RPI + g0) * 128;
     const uint32_t sw0 = ((ch ^ (pw * C::RPI + g0)) & 7) << 4, sw1 = sw0 ^ (4 << 4);
     int nk = 0;                               // K tiles copied
-    int used = 0;                             // Q stages filled
+    // test hook: the first of them (nk = 1) is left out
+    const int skip = a.lost && blockIdx.x == 0 && pw == 0 ? 1 : 0;
     while (ok && key_next(pl, w, w_end, job, pc)) {
       const int b = pc.job, i0 = pc.unit * KM_KEYS;
       const int nj = pl.kl[b] - i0 > 128 ? 2 : 1;
@@ -188,7 +190,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
                          src + (ps < 0 ? 0 : ps) * a.ld_kv, ps >= 0);
             }
             key_copy_commit();
-          } else if (lane == 0) {
+          } else if (lane == 0 && nk != skip) {
             if (pw == 0) {
               mbar_expect_tx(bar(C::B_KF), nj * C::TILE);
               for (int j = 0; j < nj; ++j)
@@ -232,12 +234,11 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::B_F + st));
         }
-        used = min(used + 1, C::NS);
         if (new_k && a.keys) {
           key_copy_wait<0>();
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::B_KF));
+          if (lane == 0 && nk != skip) mbar_arrive(bar(C::B_KF));
         }
         if (++blk == nqt) {
           blk = 0;
@@ -252,14 +253,7 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
       atomicExch(a.err, DEV_TIMEOUT_PRODUCER);
       *abort_flag = 1;
     }
-    // Every copy lands before the CTA can exit: the issuing warps have waited for
-    // each, unless a wait ran out (then here, within the limit).
-    if (pw == 0 && lane == 0 && *abort_flag) {
-      volatile int never = 0;
-      if (nk > 0) mbar_wait(bar(C::B_KF), (uint32_t)(nk - 1) & 1u, &never, lim / 2);
-      for (int s = 0; s < used; ++s)
-        mbar_wait(bar(C::B_F + s), s < st ? ph : ph ^ 1u, &never, lim / (2 * C::NS));
-    }
+    if (pw == 0 && lane == 0) *fills = KeyFills{st, (int)ph, nk};
   } else if (warp < 3) {
     // ------------------------------------------------------------- MMA
     const int j = warp - 1;                   // key tile
@@ -402,6 +396,8 @@ __global__ void __launch_bounds__(KM_THREADS, 1) key_mass_tc_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // no role can raise the flag any more
+  if (threadIdx.x == 0 && *abort_flag) key_drain(*fills, bar(C::B_F), C::NS, bar(C::B_KF), lim);
   if (warp == 1) {
     __syncwarp();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),

@@ -17,6 +17,7 @@ sl_status fail(sl_status st, const char *fmt, ...);
 sl_status cuda_fail(cudaError_t e, const char *what);
 int *device_error_word();   // per-device int, allocated on first use; nullptr on failure
 unsigned long long wait_limit_ns();   // sl_debug_set_wait_limit (0: the default)
+int take_lost_load();       // sl_debug_inject_lost_load: 1 for the one launch that loses a copy
 void note_launch(int n = 1); // count kernels launched by this library
 long long launches_total();
 
@@ -255,6 +256,7 @@ struct KeyArgs {
   int n_ctas;                     // CTAs of the launch (attention / weight)
   int *err;
   unsigned long long wait_ns;
+  int lost;                       // test hook: CTA 0 leaves out the copy of its first key tile
 };
 // Kernel attributes of this head layout on the current device.
 cudaError_t key_attn_setup(int dtype, int D);

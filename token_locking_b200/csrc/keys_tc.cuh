@@ -43,6 +43,31 @@ __device__ __forceinline__ bool key_wait(uint32_t bar, uint32_t parity, volatile
   return key_wait_long(bar, parity, abort_flag, lim);
 }
 
+// Parity of the last fill of stage s of a ring whose next fill goes to stage st in
+// the phase of parity ph.  (For a stage never filled: parity 1, for which a new
+// barrier lets its waiter pass.)
+__host__ __device__ __forceinline__ uint32_t key_ring_parity(int s, int st, uint32_t ph) {
+  return s < st ? ph : ph ^ 1u;
+}
+
+// Where warp 0's copies ended, for whoever waits for them.
+struct KeyFills {
+  int st, ph;                 // the ring's next stage and its parity
+  int n;                      // fills of the other operand's barrier
+};
+// Waits, within the limit, for the last fills of a ring of `stages` barriers and of
+// the other operand's: those of a CTA that gave up, which must land before it exits
+// (otherwise the issuing warps have waited for each).  A fill that was not handed
+// over costs its share of the limit.
+static __device__ __noinline__ void key_drain(const KeyFills &f, uint32_t ring, int stages,
+                                              uint32_t other, unsigned long long lim) {
+  volatile int never = 0;
+  if (f.n > 0) mbar_wait(other, (uint32_t)(f.n - 1) & 1u, &never, lim / 2);
+  for (int s = 0; s < stages; ++s)
+    mbar_wait(ring + 8u * (uint32_t)s, key_ring_parity(s, f.st, (uint32_t)f.ph), &never,
+              lim / (2 * stages));
+}
+
 // Keeps a branch a branch: masks turned into selects cost two instructions a
 // score in every tile, a third of the softmax's.
 __device__ __forceinline__ void key_cold() { asm volatile("" ::: "memory"); }

@@ -281,12 +281,13 @@ def device_check(clear: bool = True):
 
 
 def debug_set_wait_limit(ns: int):
-    """Barrier-wait limit of later GEMM launches in ns (0 = the default 2 s)."""
+    """Barrier-wait limit of later tensor-core launches in ns (0 = the default 2 s)."""
     A.check(A.lib().sl_debug_set_wait_limit(int(ns)), "sl_debug_set_wait_limit")
 
 
 def debug_inject_lost_load():
-    """The next 1-SM GEMM launch leaves out its first stage's copies (test hook)."""
+    """The next 1-SM GEMM, key-set attention or key weight launch leaves out its first
+    stage's copies (test hook)."""
     A.check(A.lib().sl_debug_inject_lost_load(), "sl_debug_inject_lost_load")
 
 
