@@ -61,3 +61,22 @@ def test_lost_key_tile_is_reported_and_the_next_call_exact(cuda_dev, case):
     _timeout(weigh)
     assert torch.equal(weigh(), want)
     rt.device_check(clear=True)
+
+
+def test_a_bad_position_does_not_hide_a_timeout(cuda_dev):
+    """The first report stays: a call that gave up, then one with a position outside
+    the cache, before anyone asks."""
+    c = Case(cuda_dev, "bf16", [9], [200], 256, 2, 2, 128, listed=True, seed=63)
+    ka = c.key_attention()
+    o, lse = c.outputs()
+
+    def both():
+        c.attend(ka, o, lse)                             # loses its first tile
+        c.keys[0, 7] = 256
+        c.attend(ka, o, lse)
+
+    _timeout(both)
+    c.attend(ka, o, lse)
+    with pytest.raises(A.SureLockError) as e:
+        rt.device_check(clear=True)
+    assert e.value.status == A.SL_ERR_STATE

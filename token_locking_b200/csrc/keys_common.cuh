@@ -39,7 +39,7 @@ __device__ __forceinline__ int key_pos(const KeyArgs &a, int b, int i) {
   if (!a.keys) return i;
   const int n = a.keys[(size_t)b * a.n_ctx + i];
   if ((unsigned)n < (unsigned)a.n_ctx) return n;
-  atomicExch(a.err, DEV_BAD_INDEX);
+  atomicCAS(a.err, DEV_OK, DEV_BAD_INDEX);    // an earlier report stays
   return -1;
 }
 
