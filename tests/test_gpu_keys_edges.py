@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from keys_util import Case, ref_mass
+from keys_util import Case, ref_attend, ref_evict, ref_mass
 from token_locking_b200 import _abi as A
 from token_locking_b200 import runtime as rt
 
@@ -94,3 +94,110 @@ def test_budgets_beyond_32_bits(cuda_dev):
         with pytest.raises(A.SureLockError) as e:
             rt.kv_evict(m, budget, keys, n)
         assert e.value.status == A.SL_ERR_INVALID
+
+
+# Work plans that the other shapes do not reach (on 148 SMs): shares long enough to be
+# padded to each sequence's start, and a joint prefix whose units are dealt out whole.
+PLANS = [
+    ("bf16", [61, 102, 143, 218, 82], [539, 371, 71, 426, 189], 540, 6, 6, 128, 12414),
+    ("bf16", [271, 259, 111, 108, 107], [217, 353, 212, 459, 420], 460, 6, 6, 64, 11142),
+    ("bf16", [20, 20, 20], [240, 240, 240], 240, 37, 37, 128, 240),
+    ("bf16", [20, 20, 20], [240, 240, 240], 240, 74, 74, 128, 240),
+    ("f32", [8, 8, 8], [192, 192, 192], 192, 74, 74, 16, 192),
+]
+
+
+@pytest.mark.parametrize("shape", PLANS, ids=lambda s: "-".join(map(str, s)).replace(" ", ""))
+def test_padded_shares_and_whole_joint_units(cuda_dev, shape):
+    dtype, counts, lens, n_ctx, H, Hk, dh, prefix = shape
+    c = Case(cuda_dev, dtype, counts, lens, n_ctx, H, Hk, dh, prefix, seed=54, extra_rows=2)
+    c.poison()
+    ka = c.key_attention()
+    o, lse = c.outputs()
+    c.attend(ka, o, lse)
+    ro, bo, rl, bl = ref_attend(c)
+    end = int(c.off[-1])
+    assert (o[end:] == 7).all() and (lse[end:] == 7).all()
+    assert _within(o[:end], ro[:end], bo[:end]) and _within(lse[:end], rl[:end], bl[:end])
+    o2, lse2 = c.outputs()
+    c.attend(ka, o2, lse2)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_two_objects_at_the_same_time(cuda_dev):
+    """Two objects, each on a stream of its own, nothing ordering them."""
+    cs = [Case(cuda_dev, "bf16", [90, 300], [700, 300], 700, 4, 4, 128, prefix=p, listed=not p,
+               seed=55) for p in (0, 333)]
+    kas, want = [c.key_attention() for c in cs], []
+
+    def both(c, ka, stream):
+        with torch.cuda.stream(stream):
+            o, lse = c.outputs()
+            m = torch.empty((2, 700), device=cuda_dev)
+            c.attend(ka, o, lse)
+            ka.mass(c.q, c.k, lse, m, c.seq_off, key_len=c.key_len, keys=c.keys)
+            return o, lse, m
+
+    for c, ka in zip(cs, kas):
+        want.append(both(c, ka, torch.cuda.current_stream()))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [both(c, ka, s) for c, ka, s in zip(cs, kas, streams)]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+    rt.device_check()
+
+
+def _evicts(dev, mass, budget, protect, present):
+    B, N = mass.shape
+    keys = torch.full((B, N), -9, dtype=torch.int32, device=dev)
+    n = torch.full((B,), -9, dtype=torch.int32, device=dev)
+    out = torch.full((B, N), 9, dtype=torch.uint8, device=dev)
+    rt.kv_evict(mass, budget, keys, n, protect=protect, present=present, present_out=out)
+    for b, want in enumerate(ref_evict(mass.cpu().numpy(), budget, protect.cpu().numpy(),
+                                       present.cpu().numpy())):
+        flags = torch.zeros(N, dtype=torch.uint8)
+        flags[want] = 1
+        assert n[b] == len(want)
+        assert keys[b, :len(want)].tolist() == want and (keys[b, len(want):] == -9).all()
+        assert torch.equal(out[b].cpu(), flags)
+
+
+@pytest.mark.parametrize("N", [4095, 4096, 4097, 8192, 8193, 12001, 16384, 16385, 393216, 393217])
+def test_evict_at_the_borders_of_its_clusters(cuda_dev, N):
+    """One, two, four and eight CTAs a sequence, entries kept in shared memory or read
+    again, each side of every border."""
+    g = torch.Generator(device=cuda_dev).manual_seed(N)
+    B = 1 if N > 20000 else 2
+    m = torch.exp(2 * torch.randn((B, N), device=cuda_dev, generator=g))
+    ties = torch.randint(-1, 3, (B, N), device=cuda_dev, generator=g).float()
+    protect = (torch.rand((B, N), device=cuda_dev, generator=g) < 0.1).to(torch.uint8)
+    present = (torch.rand((B, N), device=cuda_dev, generator=g) < 0.8).to(torch.uint8)
+    _evicts(cuda_dev, m, N // 2, protect, present)
+    _evicts(cuda_dev, ties, N // 3, protect, present)
+
+
+def test_captured_eviction_follows_new_weights(cuda_dev):
+    B, N = 2, 9000
+    m = torch.rand((B, N), device=cuda_dev)
+    present = torch.ones((B, N), dtype=torch.uint8, device=cuda_dev)
+    keys = torch.zeros((B, N), dtype=torch.int32, device=cuda_dev)
+    n = torch.zeros(B, dtype=torch.int32, device=cuda_dev)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            rt.kv_evict(m, 1000, keys, n, present=present, present_out=present)
+        for seed in range(3):
+            g = torch.Generator(device=cuda_dev).manual_seed(seed)
+            m.copy_(torch.randn((B, N), device=cuda_dev, generator=g))
+            present.copy_((torch.rand((B, N), device=cuda_dev, generator=g) < 0.5).to(torch.uint8))
+            was = present.cpu().numpy()
+            graph.replay()
+            st.synchronize()
+            for b, want in enumerate(ref_evict(m.cpu().numpy(), 1000, None, was)):
+                assert n[b] == len(want) and keys[b, :len(want)].tolist() == want
+                assert present[b].nonzero()[:, 0].tolist() == want
