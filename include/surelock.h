@@ -443,7 +443,7 @@ void sl_sampler_destroy(sl_sampler *s);
  * decode and let each active row attend to all N of them (Paper-Notes,
  * "permanent locking"; gist.science/nl section 2, O(M N d)); these entry points
  * are library-level: they cut N to the entries that are still looked at, and
- * read a prompt shared by the batch once.  They take pointers to any cache of
+ * can read a prompt shared by the batch once.  They take pointers to any cache of
  * [batch * n_ctx][ld] rows (sl_kv_cache_view gives such pointers), with K/V
  * heads that several query heads may share.
  *
@@ -463,8 +463,11 @@ typedef struct sl_key_attn_config {
   float scale;           /* score scale; 0 = 1 / sqrt(head_dim) */
 } sl_key_attn_config;
 /* SL_ERR_INVALID / SL_ERR_UNSUPPORTED on sizes outside the above, SL_ERR_OOM if
- * the workspace cannot be allocated (about 40 MB for bf16 heads of 128, and with
- * `prefix` 1 KB more per row and head for up to 96 * batch rows). */
+ * the workspace cannot be allocated.  It is the larger of what attention takes
+ * (about 40 MB for bf16 heads of 128, and with `prefix` 8 * head_dim + 16 bytes more
+ * per query head and row for up to 96 * batch * n_kv_heads / n_heads rows) and what
+ * the weights take (about 1 MB, and 8 bytes per cache row for bf16 heads of 64 and
+ * 128, 4 bytes otherwise). */
 sl_status sl_key_attn_create(const sl_key_attn_config *cfg, sl_key_attn **out);
 void sl_key_attn_destroy(sl_key_attn *a);
 
@@ -485,7 +488,12 @@ typedef struct sl_key_set {
 /*   o_jh = sum_n p_jhn v_n,  p_jhn = exp(scale q_jh . k_n - lse_jh),
  *   lse_jh = log sum_n exp(scale q_jh . k_n)
  * over the prefix_len rows of the prefix (shared by every sequence) and the
- * row's key set.  q, o: [rows][ld >= n_heads * head_dim]; k, v:
+ * row's key set.  Up to 96 * batch * n_kv_heads / n_heads rows the prefix may be
+ * passed over once for the rows of all sequences; above, or where that costs more,
+ * each sequence's rows run through it.  The caller sees to it that the prefix's keys
+ * fit the rows': in their positions (the keys that sl_step writes count from 0 in
+ * every sequence, with no offset for a prompt before them) and as a prompt encoded
+ * on its own (attention within a sequence is bidirectional).  q, o: [rows][ld >= n_heads * head_dim]; k, v:
  * [batch * n_ctx][ld_kv >= n_kv_heads * head_dim]; prefix: [prefix_len][ld_prefix];
  * pointers and rows 16-byte aligned.  d_lse [rows][n_heads] fp32, or NULL.  A row
  * without keys, or with scores of -inf only, gets o = 0, lse = -inf; rows outside
@@ -503,7 +511,8 @@ sl_status sl_key_attention(sl_key_attn *a, int rows, const void *d_q, int64_t ld
  * mass_prev: [batch][n_ctx] fp32, may be the same; decay = 0 does not read
  * mass_prev (may be NULL).  Rows with lse = -inf weigh nothing, whatever their q
  * holds.  The same call gives the same bits, unless a list names a position more
- * than once (its weights are then added in no fixed order). */
+ * than once (its weights are then added in no fixed order).  Sums in fp32; bf16
+ * heads of 64 and 128 take exponentials of 2^-22 relative error. */
 sl_status sl_key_mass(sl_key_attn *a, int rows, const void *d_q, int64_t ld_q, const void *d_k,
                       int64_t ld_kv, const sl_key_set *set, const float *d_lse, float decay,
                       const float *d_mass_prev, float *d_mass, void *stream);
@@ -540,9 +549,9 @@ sl_status sl_timing_read(sl_model *m, sl_timing *out, int reset);
 
 /* Device error word, set by a kernel that gave up a bounded wait or met a
  * token id outside [0, vocab) or a listed key position outside [0, n_ctx) (that
- * row is embedded, that key taken, as zeros, never read from out of range): returns SL_ERR_TIMEOUT or SL_ERR_STATE respectively (and
- * clears the word if `clear`), SL_OK if nothing was recorded.  Synchronises
- * the device. */
+ * row is embedded, that key taken, as zeros, never read from out of range):
+ * returns SL_ERR_TIMEOUT or SL_ERR_STATE respectively (and clears the word if
+ * `clear`), SL_OK if nothing was recorded.  Synchronises the device. */
 sl_status sl_device_check(int clear);
 
 /* Test hooks for the failure path of the bounded waits.  Neither raises a GPU

@@ -218,8 +218,11 @@ __global__ void __launch_bounds__(KS_THREADS) key_attn_simt_kernel(const KeyArgs
 // units that a CTA's share cut have partial rows: blockIdx.x = c looks at the
 // cut at the start of CTA c's share, and the first cut of a unit joins it,
 // blockIdx.y sharing its rows.  With one, every row does (one part from the
-// prefix, one from its sequence's own keys).  All blocks fit the GPU at once
-// (twice as many took 16 us of 48 at 300 rows and 32 heads a sequence).
+// prefix, one from its sequence's own keys).  After a launch of one CTA per SM all
+// blocks fit the GPU at once (twice as many took 16 us of 48 at 300 rows and 32
+// heads a sequence); after one of two per SM (fp32 arithmetic, heads up to 64) they
+// come in two rounds.  64 registers let four blocks share an SM and spill 164 bytes
+// a thread.
 constexpr int KJ_WARPS = 8, KJ_Y = 4;         // warps of a block, blocks per cut
 struct JoinAcc {
   float m, l;
@@ -506,6 +509,7 @@ cudaError_t launch_key_join(const KeyArgs &a, int rt, int uq, cudaStream_t s) {
                         by_uq);
 }
 
+// Shares of one tile: see the kernel (24 us against 36 with two).
 cudaError_t launch_key_attn(KeyArgs a, cudaStream_t s) {
   if (key_attn_tc_takes(a.dtype, a.D)) return launch_key_attn_tc(a, s);
   a.ov = 1;

@@ -16,8 +16,11 @@
 //                2^(s scale log2(e) - lse log2(e)) over half of a block's rows
 // A product takes 512 clocks and its 128 x 128 exponentials 1024, so the
 // exponentials bound the kernel: 4 sequences of 2048 rows, keys and 32 heads take
-// 185 us, the special-function unit busy 79 % of the time.  (A quarter of the
-// exponentials by a polynomial on the FMA pipe: 195 us, under the power limit.)
+// 184 to 190 us (two cards), the special-function unit busy 78 % of the time.  (A quarter of the
+// exponentials by a polynomial on the FMA pipe: 5 % more, under the power limit.)
+// They are the unit's own 2^x (2^-22 relative error), four times the plain form's
+// error and far below the scores' rounding.  With a list the rows of a head's keys
+// are copied one by one into the one K buffer: 201 us, 112 against 99 for 1024 keys.
 // The K tiles need one buffer only: when a head's products are done, the score
 // buffers hold work for longer than the next head's copy takes.
 #include <string.h>
@@ -433,6 +436,8 @@ cudaError_t key_mass_tc_setup(int D) {
                                          KmCfg<64>::SMEM);
 }
 
+// Least share of a CTA, in tile times: with 1 / 2 / 4 the weights of a window of 200
+// rows over 384 keys take 17.9 / 15.3 / 16.4 us, longer calls the same.
 cudaError_t launch_key_mass_tc(KeyArgs a, cudaStream_t s) {
   a.ov = 1;
   a.min_chunk = 2;

@@ -257,13 +257,17 @@ __global__ void __launch_bounds__(EV_THREADS) evict_kernel(
   cluster_sync();                            // no CTA leaves while another reads its counts
 }
 
+// The longest that is offered: its eight CTAs read 2^17 entries each in every pass.
 int evict_max_ctx() { return 1 << 20; }
 
 cudaError_t launch_evict(int batch, int n_ctx, int budget, const float *mass,
                          const uint8_t *protect, const uint8_t *present, int32_t *keys,
                          int32_t *key_len, uint8_t *present_out, cudaStream_t s) {
-  // one CTA up to four entries a thread: a cluster's exchanges cost more than
-  // they share out; beyond that the largest portable cluster
+  // CTAs a sequence by entries a thread: a cluster's exchanges cost about what it
+  // shares out at four (4 sequences, with 1 / 2 / 4 / 8 CTAs each: 2048 entries 9.2 /
+  // 8.9 / 8.9 / 9.7 us, 4096 10.3 / 9.7 / 9.1 / 9.9, 8192 12.7 / 10.7 / 9.8 / 10.1,
+  // 12000 12.7 / 9.4 / 7.9 / 8.4, 16384 14.7 / 10.3 / 8.1 / 8.0, 24000 19.6 / 12.9 /
+  // 9.5 / 8.7); beyond that the largest portable cluster
   const int cs = n_ctx <= 4 * EV_THREADS ? 1 : n_ctx <= 8 * EV_THREADS ? 2
                  : n_ctx <= 16 * EV_THREADS ? 4 : EV_CLUSTER;
   const int seg = (n_ctx + cs - 1) / cs, cached = seg <= EV_CACHE;

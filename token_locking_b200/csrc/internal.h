@@ -231,7 +231,10 @@ cudaError_t launch_gemm_tc(const TcGemmArgs &a, int num_sms, int *err, cudaStrea
 // ------------------------------------------------- attn_keys.cu, attn_mass.cu
 // Attention over a key set per sequence, and the attention weight each key
 // receives (see keys_plan.cuh for how the work is shared out).
-constexpr int KP_JOIN_NUM = 1, KP_JOIN_DEN = 16;   // joining one packed row, in tile times
+// Joining one packed row, in tile times: what a joint prefix costs beside what it
+// saves.  From 1/64 to 1/4 the same plans result over long prefixes; 16 x 64 rows over
+// a prefix of 500 keys take 81 us with 1/64 and 1/16, 56 with 1/4 (no joint prefix).
+constexpr int KP_JOIN_NUM = 1, KP_JOIN_DEN = 16;
 constexpr int KEY_PLAN_WORDS = 512;
 // Most query rows, cache rows (batch * n_ctx) and prefix rows of a call: they are
 // counted in 32 bits, and tiles (256 rows) and grid strides (1024 blocks of 32

@@ -199,7 +199,7 @@ __device__ __forceinline__ int kp_job_at(const KeyPlan &pl, const int *base, int
 // CTA c's share: virtual tiles [w, w_end), or where shares are whole units, units
 // w, w + n_ctas, ... below w_end, so that the CTAs work on neighbouring units at a
 // time and a head's keys come from memory once (a run of neighbouring units per
-// CTA read 714 MB for 168 at 4 x 2048 rows over 1536 keys, 298 us instead of 252).
+// CTA read 714 MB for 168 at 4 x 2048 rows over 1536 keys, in 1.18 times the time).
 __device__ __forceinline__ void key_begin(const KeyPlan &pl, int c, int lane, int &w, int &w_end,
                                           int &job) {
   const int W = pl.wbase[pl.njobs];
