@@ -16,11 +16,12 @@
 //                2^(s scale log2(e) - lse log2(e)) over half of a block's rows
 // A product takes 512 clocks and its 128 x 128 exponentials 1024, so the
 // exponentials bound the kernel: 4 sequences of 2048 rows, keys and 32 heads take
-// 184 to 190 us (two cards), the special-function unit busy 78 % of the time.  (A quarter of the
-// exponentials by a polynomial on the FMA pipe: 5 % more, under the power limit.)
-// They are the unit's own 2^x (2^-22 relative error), four times the plain form's
-// error and far below the scores' rounding.  With a list the rows of a head's keys
-// are copied one by one into the one K buffer: 201 us, 112 against 99 for 1024 keys.
+// 184 to 190 us (two cards), the special-function unit busy 78 % of the time.  (A
+// quarter of the exponentials by a polynomial on the FMA pipe: 5 % more, under the
+// power limit.)  They are the unit's own 2^x (2^-22 relative error), four times the
+// plain form's error and far below the scores' rounding.  With a list the rows of a
+// head's keys are copied one by one into the one K buffer: 201 us, and 112 against
+// 99 for 1024 keys.
 // The K tiles need one buffer only: when a head's products are done, the score
 // buffers hold work for longer than the next head's copy takes.
 #include <string.h>
